@@ -397,6 +397,67 @@ nvfp4moe_status moe_ffn_forward(const moe_ffn_desc* desc, const void* x, const f
                                 nvfp4moe_stream_t stream);
 
 /* ------------------------------------------------------------------------------
+ * FP8 with a scale for each block of 128.  (The pages describe NVFP4 experts only; this is the
+ * 8-bit form of the same layer, for checkpoints that keep their experts in E4M3.)
+ *
+ *   value = e4m3(code) * fp32 scale, one scale per group of 128:
+ *     activations  1 x 128:   one row, 128 consecutive elements along K
+ *     weights      128 x 128: 128 rows and 128 columns
+ *   scale = amax / 448 of the group rounded to fp32; code = the E4M3 value nearest to the real
+ *   quotient x / scale (ties to even, saturating).  A group of zeros has scale 0 and codes 0; a
+ *   group with a NaN has scale NaN and NaN codes; one with an infinity has an infinite scale.
+ * Groups at the end of a row or matrix are shorter: there is a scale for each begun group.
+ * Codes are row-major bytes, scales row-major fp32 [rows or ceil(rows/128)][ceil(K/128)].
+ *
+ * fp8_quantize - bf16 / fp32 -> E4M3 and scales.  x [batch][rows][K] (row pitch ldx and batch
+ * stride in elements), codes [batch][rows][K] (pitch ldc, bytes), scale (pitch lds, elements).
+ * tile: NVFP4MOE_FP8_ROWS (1 x 128) or NVFP4MOE_FP8_BLOCKS (128 x 128).  Any sizes and pitches;
+ * 16-byte aligned rows of x and 8-byte aligned rows of codes are read and written widest.  Bytes
+ * of codes between K and the pitch are left as they are.
+ *
+ * fp8_gemm - D[M][N] = A . B^T: A [M][K] with 1 x 128 scales, B [N][K] with 128 x 128 scales, D
+ * bf16 or fp32 (d_dtype).  Products of one 128-block of K are summed in fp32 by the tensor cores,
+ * multiplied by the block's two scales and added in fp32.  Row pitches: lda, ldb in bytes
+ * (multiples of 16, as the base addresses), lda_s, ldb_s, ldd in elements.  M, N, K >= 1 of any
+ * size (M or N of 0: nothing to do).  No workspace; the result does not depend on timing.
+ * ---------------------------------------------------------------------------- */
+enum { NVFP4MOE_FP8_ROWS = 0, NVFP4MOE_FP8_BLOCKS = 1 };
+
+nvfp4moe_status fp8_quantize(const void* x, int32_t x_dtype, int64_t batch, int64_t rows, int64_t K,
+                             int64_t ldx, int64_t x_batch_stride, int32_t tile, uint8_t* codes,
+                             int64_t ldc, int64_t codes_batch_stride, float* scale, int64_t lds,
+                             int64_t scale_batch_stride, nvfp4moe_stream_t stream);
+
+nvfp4moe_status fp8_gemm(const uint8_t* A, int64_t lda, const float* A_scale, int64_t lda_s,
+                         const uint8_t* B, int64_t ldb, const float* B_scale, int64_t ldb_s, int64_t M,
+                         int64_t N, int64_t K, void* D, int64_t ldd, int32_t d_dtype,
+                         nvfp4moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------
+ * fp8_moe_ffn_forward - the routed feed-forward layer on FP8 weights:
+ *   ids, w = top-k of the logits and the softmax over them (as moe_route)
+ *   xq     = FP8(x), 1 x 128 groups
+ *   h      = FP8(silu(xq . Wg[e]^T) * (xq . Wu[e]^T)), 1 x 128 groups of the fp32 products
+ *   out[t] = bf16(sum_j w[t][j] * (h . Wd[e]^T)), fp32, in slot order
+ * x bf16 [T][H], logits fp32 [T][E] (finite), out bf16 [T][H]; all contiguous, x, out and the
+ * weights 16-byte aligned, the workspace 256-byte aligned.  H and I: multiples of 16; E <= 1024,
+ * 1 <= top_k <= min(E, 32), T * top_k <= 2^24.  Nothing in the workspace is read before the call
+ * writes it; calls that share one must be ordered.  Deterministic.
+ * ---------------------------------------------------------------------------- */
+typedef struct {
+  int32_t T, H, I, E, top_k;
+  const uint8_t* w13_codes; /* [E][2][I][H]: gate, then up */
+  const float* w13_scale;   /* [E][2][ceil(I/128)][ceil(H/128)] */
+  const uint8_t* w2_codes;  /* [E][H][I] */
+  const float* w2_scale;    /* [E][ceil(H/128)][ceil(I/128)] */
+} fp8_moe_ffn_desc;
+
+size_t fp8_moe_ffn_workspace_size(const fp8_moe_ffn_desc* d); /* 0: a size is not supported */
+nvfp4moe_status fp8_moe_ffn_forward(const fp8_moe_ffn_desc* desc, const void* x, const float* logits,
+                                    void* out, void* workspace, size_t workspace_bytes,
+                                    nvfp4moe_stream_t stream);
+
+/* ------------------------------------------------------------------------------
  * Measurement and self-test entry points.  The pages have no counterpart of these: they
  * measure the device and exercise the library's failure reporting, and compute nothing of
  * the layer.

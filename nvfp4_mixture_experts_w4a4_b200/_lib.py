@@ -18,6 +18,7 @@ PATH_AUTO, PATH_GEMV, PATH_GEMM = 0, 1, 2
 COMBINE_AUTO, COMBINE_ORDERED, COMBINE_ACCUMULATE = 0, 1, 2
 ACT_NVFP4, ACT_BF16 = 0, 1
 LAUNCH_AUTO, LAUNCH_SINGLE, LAUNCH_MULTI, LAUNCH_SINGLE_TILE, LAUNCH_SINGLE_LOCAL = 0, 1, 2, 3, 4
+FP8_ROWS, FP8_BLOCKS = 0, 1
 STAGES = 7
 STAGE_NAMES = ("route", "permute", "quantize_x", "gate_up", "down", "combine")
 DEV_BAD_EXPERT_ID, DEV_DUPLICATE_ID, DEV_ROW_OVERFLOW, DEV_TIMEOUT, DEV_BAD_GATHER = 1, 2, 4, 8, 16
@@ -60,6 +61,13 @@ class MoeFfnWsLayout(ctypes.Structure):
         ("h_bf16", _i64), ("shared_h", _i64), ("shared_y", _i64)]
 
 
+class Fp8MoeFfnDesc(ctypes.Structure):
+    _fields_ = [
+        ("T", _i32), ("H", _i32), ("I", _i32), ("E", _i32), ("top_k", _i32),
+        ("w13_codes", _vp), ("w13_scale", _vp), ("w2_codes", _vp), ("w2_scale", _vp),
+    ]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "nvfp4moe_last_error": (ctypes.c_char_p, []),
@@ -83,6 +91,10 @@ SIGNATURES = {
     "moe_ffn_workspace_layout": (_i32, [ctypes.POINTER(MoeFfnDesc), ctypes.POINTER(MoeFfnWsLayout)]),
     "moe_ffn_workspace_size": (_sz, [ctypes.POINTER(MoeFfnDesc)]),
     "moe_ffn_forward": (_i32, [ctypes.POINTER(MoeFfnDesc), _vp, _vp, _vp, _vp, _sz, _vp]),
+    "fp8_quantize": (_i32, [_vp, _i32, _i64, _i64, _i64, _i64, _i64, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _vp]),
+    "fp8_gemm": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _i32, _vp]),
+    "fp8_moe_ffn_workspace_size": (_sz, [ctypes.POINTER(Fp8MoeFfnDesc)]),
+    "fp8_moe_ffn_forward": (_i32, [ctypes.POINTER(Fp8MoeFfnDesc), _vp, _vp, _vp, _vp, _sz, _vp]),
     "nvfp4moe_mma_peak_probe": (_i32, [_i64, _vp]),
     "nvfp4moe_mma_peak_probe_flops": (_i64, [_i64]),
     "nvfp4moe_wait_selftest": (_i32, [ctypes.c_uint32, _vp, _vp]),

@@ -1,0 +1,189 @@
+// fp8_moe_ffn_forward: the routed feed-forward layer on FP8 weights with a scale per 128 x 128
+// block.  Routing and permutation are the NVFP4 layer's (one order for both), x is quantised per
+// row and 128 columns into expert order, and the products run in fp8_tile.cu.
+#include "ffn_gemv.cuh"
+#include "fp8.cuh"
+#include "fp8_tile.cuh"
+
+namespace nvfp4moe {
+namespace {
+
+constexpr int kPlaceThreads = 256;
+constexpr int kRowTile = 128;
+
+// x [T][H] bf16 -> E4M3 rows in expert order: each 128-element group is quantised once (half a
+// warp, 16 bytes a lane) and written to the k rows of its token.  Block 0 writes the list of row
+// tiles instead: {expert, first row, rows} for every 128 rows of every expert, [0].x their number.
+__global__ void __launch_bounds__(kPlaceThreads)
+fp8_place_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ pair_to_row,
+                 const int32_t* __restrict__ offsets, int T, int H, int E, int k, uint8_t* __restrict__ codes,
+                 float* __restrict__ scale, int4* __restrict__ tiles) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x == 0) {
+    __shared__ int s_sum[kPlaceThreads / 32];
+    constexpr int PER = 1024 / kPlaceThreads;
+    const int e0 = threadIdx.x * PER;
+    int first[PER], n[PER], mine = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = e0 + i;
+      first[i] = e < E ? offsets[e] : 0;
+      n[i] = e < E ? offsets[e + 1] - first[i] : 0;
+      mine += (n[i] + kRowTile - 1) / kRowTile;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    int at = incl - mine, total = 0;
+    for (int w = 0; w < kPlaceThreads / 32; ++w) {
+      if (w < warp) at += s_sum[w];
+      total += s_sum[w];
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      for (int r = 0; r < n[i]; r += kRowTile) tiles[1 + at++] = make_int4(e0 + i, first[i] + r, min(kRowTile, n[i] - r), 0);
+    if (threadIdx.x == 0) tiles[0] = make_int4(total, 0, 0, 0);
+    return;
+  }
+  const int nb = (H + FP8_BLOCK - 1) / FP8_BLOCK;
+  const int64_t groups = int64_t(T) * nb;
+  const int64_t g = (int64_t(blockIdx.x - 1) * kPlaceThreads + threadIdx.x) / 16;
+  const int sub = threadIdx.x & 15;
+  const int64_t t = g / nb;
+  const int b = int(g - t * nb), c = b * FP8_BLOCK + sub * 8;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  const bool live = g < groups && c < H;  // H is a multiple of 16: eight elements exist or none
+  if (live) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + t * H + c));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const Fp8Scale f = fp8_scale(m);
+  const uint2 out = make_uint2(fp8_encode4(v, f), fp8_encode4(v + 4, f));
+  if (!live) return;
+  for (int j = 0; j < k; ++j) {
+    const int64_t row = __ldg(pair_to_row + t * k + j);
+    *reinterpret_cast<uint2*>(codes + row * H + c) = out;
+    if (sub == 0) scale[row * nb + b] = f.scale;
+  }
+}
+
+struct Layout {
+  int64_t ids, w, counts, offsets, padded, pair_to_row, row_token, row_pair, tile_expert, active, scratch, tiles,
+      x_codes, x_scale, h_codes, h_scale, slots, total;
+  int64_t pairs;
+  int max_row_tiles;
+};
+
+nvfp4moe_status check_desc(const fp8_moe_ffn_desc* d, const char* fn) {
+  NVFP4_REQUIRE(d != nullptr, NVFP4MOE_INVALID_ARG, "%s: NULL descriptor", fn);
+  NVFP4_REQUIRE(d->T >= 0, NVFP4MOE_INVALID_ARG, "%s: T < 0", fn);
+  NVFP4_REQUIRE(d->H >= 16 && d->H % 16 == 0 && d->H <= (1 << 20), NVFP4MOE_UNSUPPORTED_SHAPE,
+                "%s: H=%d is not a multiple of 16 in [16, 2^20]", fn, d->H);
+  NVFP4_REQUIRE(d->I >= 16 && d->I % 16 == 0 && d->I <= (1 << 20), NVFP4MOE_UNSUPPORTED_SHAPE,
+                "%s: I=%d is not a multiple of 16 in [16, 2^20]", fn, d->I);
+  NVFP4_REQUIRE(d->E >= 1 && d->E <= 1024, NVFP4MOE_UNSUPPORTED_SHAPE, "%s: E=%d outside [1, 1024]", fn, d->E);
+  NVFP4_REQUIRE(d->top_k >= 1 && d->top_k <= 32 && d->top_k <= d->E, NVFP4MOE_UNSUPPORTED_SHAPE,
+                "%s: top_k=%d outside [1, min(E, 32)]", fn, d->top_k);
+  NVFP4_REQUIRE(int64_t(d->T) * d->top_k <= (int64_t(1) << 24), NVFP4MOE_UNSUPPORTED_SHAPE, "%s: T*top_k > 2^24", fn);
+  return NVFP4MOE_OK;
+}
+
+Layout make_layout(const fp8_moe_ffn_desc& d) {
+  Layout L{};
+  int64_t at = 0;
+  auto put = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  const int64_t P = int64_t(d.T) * d.top_k, nH = fp8_blocks(d.H), nI = fp8_blocks(d.I);
+  L.pairs = P;
+  L.max_row_tiles = int(P / kRowTile + (P < d.E ? P : d.E));
+  L.ids = put(P * 4), L.w = put(P * 4);
+  L.counts = put(d.E * 4), L.offsets = put((d.E + 1) * 4), L.padded = put((d.E + 1) * 4);
+  L.pair_to_row = put(P * 4), L.row_token = put(P * 4), L.row_pair = put(P * 4), L.tile_expert = put(P * 4);
+  L.active = put((d.E + 1) * 4);
+  L.scratch = put(d.T > 0 ? batch_prologue_scratch_bytes(d.T, d.E) : 0);
+  L.tiles = put((int64_t(L.max_row_tiles) + 1) * 16);
+  L.x_codes = put(P * d.H), L.x_scale = put(P * nH * 4);
+  L.h_codes = put(P * d.I), L.h_scale = put(P * nI * 4);
+  L.slots = put(P * d.H * 4);
+  L.total = at;
+  return L;
+}
+
+}  // namespace
+}  // namespace nvfp4moe
+
+using namespace nvfp4moe;
+
+extern "C" {
+
+size_t fp8_moe_ffn_workspace_size(const fp8_moe_ffn_desc* d) {
+  if (check_desc(d, "fp8_moe_ffn_workspace_size") != NVFP4MOE_OK) return 0;
+  return size_t(make_layout(*d).total);
+}
+
+nvfp4moe_status fp8_moe_ffn_forward(const fp8_moe_ffn_desc* desc, const void* x, const float* logits, void* out,
+                                    void* workspace, size_t workspace_bytes, nvfp4moe_stream_t stream) {
+  const char* fn = "fp8_moe_ffn_forward";
+  nvfp4moe_status st = check_desc(desc, fn);
+  if (st != NVFP4MOE_OK) return st;
+  const fp8_moe_ffn_desc& d = *desc;
+  if (d.T == 0) return NVFP4MOE_OK;
+  NVFP4_REQUIRE(x && logits && out && workspace, NVFP4MOE_INVALID_ARG, "%s: NULL pointer", fn);
+  NVFP4_REQUIRE(d.w13_codes && d.w13_scale && d.w2_codes && d.w2_scale, NVFP4MOE_INVALID_ARG, "%s: NULL weights", fn);
+  NVFP4_REQUIRE(aligned16(x) && aligned16(out) && aligned16(d.w13_codes) && aligned16(d.w2_codes) &&
+                    reinterpret_cast<uintptr_t>(workspace) % 256 == 0,
+                NVFP4MOE_INVALID_ARG, "%s: x, out and the weights need 16-byte alignment, the workspace 256", fn);
+  const Layout L = make_layout(d);
+  NVFP4_REQUIRE(workspace_bytes >= size_t(L.total), NVFP4MOE_WORKSPACE_TOO_SMALL, "%s: workspace %zu < %zu", fn,
+                workspace_bytes, size_t(L.total));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  auto i32 = [&](int64_t at) { return reinterpret_cast<int32_t*>(ws + at); };
+  auto f32 = [&](int64_t at) { return reinterpret_cast<float*>(ws + at); };
+  st = launch_batch_prologue(x, logits, d.T, d.H, d.E, d.top_k, 1, 0, nullptr, i32(L.ids), f32(L.w), i32(L.counts),
+                             i32(L.offsets), i32(L.padded), i32(L.pair_to_row), i32(L.row_token), i32(L.row_pair),
+                             i32(L.tile_expert), i32(L.active), nullptr, 1, nullptr, nullptr, ws + L.scratch, nullptr,
+                             nullptr, s);
+  if (st != NVFP4MOE_OK) return st;
+  int4* tiles = reinterpret_cast<int4*>(ws + L.tiles);
+  const int64_t groups = int64_t(d.T) * fp8_blocks(d.H);
+  const cudaError_t e = launch_dependent(fp8_place_kernel, dim3(unsigned(1 + (groups * 16 + kPlaceThreads - 1) / kPlaceThreads)),
+                                         dim3(kPlaceThreads), 0, s, static_cast<const __nv_bfloat16*>(x),
+                                         static_cast<const int32_t*>(i32(L.pair_to_row)),
+                                         static_cast<const int32_t*>(i32(L.offsets)), int(d.T), int(d.H), int(d.E),
+                                         int(d.top_k), ws + L.x_codes, f32(L.x_scale), tiles);
+  NVFP4_REQUIRE(e == cudaSuccess, NVFP4MOE_CUDA_ERROR, "%s: %s", fn, cudaGetErrorString(e));
+  GroupedArgs g{};
+  g.H = d.H, g.I = d.I, g.E = d.E;
+  g.rows = L.pairs;
+  g.max_row_tiles = L.max_row_tiles;
+  g.tiles = tiles;
+  g.x_codes = ws + L.x_codes, g.x_scale = f32(L.x_scale);
+  g.w13_codes = d.w13_codes, g.w13_scale = d.w13_scale, g.w2_codes = d.w2_codes, g.w2_scale = d.w2_scale;
+  g.h_codes = ws + L.h_codes, g.h_scale = f32(L.h_scale), g.slots = f32(L.slots);
+  st = launch_fp8_grouped(g, s);
+  if (st != NVFP4MOE_OK) return st;
+  return launch_combine_rows(f32(L.slots), i32(L.pair_to_row), f32(L.w), d.T, d.H, d.top_k, out, s);
+}
+
+}  // extern "C"

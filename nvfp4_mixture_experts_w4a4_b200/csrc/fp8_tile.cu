@@ -1,0 +1,647 @@
+// FP8 x FP8 products with a scale per block of 128, on the tensor cores: one dense GEMM
+// (fp8_gemm) and the grouped gate/up and down products of the routed layer.
+//
+//   D[m][n] = sum over kb of sa[m][kb] * sb[n / 128][kb] * sum over k in block kb of A[m][k] B[n][k]
+//
+// The tensor core sums one 128-element block of K (four tcgen05.mma kind::f8f6f4 of K = 32, fp32
+// accumulators in TMEM); between blocks the partial sum is multiplied by its two scales and added
+// to fp32 registers.  The rows of A are the MMA's M side, so a thread of the adding warps holds one
+// row: both scales are one number a thread, and the multiply-add is one packed FMA for two columns.
+// Two TMEM accumulators of BN columns alternate, so the MMA of block kb + 1 runs under the
+// additions of block kb.  Per block an SM multiplies for 512 cycles (128 x 256 x 128 at 8192 MACs a
+// cycle) while its eight adding warps read 128 KB of TMEM (256 cycles) and issue 64 packed FMAs a
+// thread (256 cycles a scheduler).
+//
+//   warp 0      TMA producer: 128 rows of A and BN rows of B, 128 bytes of K each, per stage
+//   warp 1      TMEM owner and MMA issuer
+//   warps 4..11 additions and epilogue: warp w reads TMEM lanes 32 * (w % 4), the first four take
+//               the left half of the columns and the others the right half
+// A thread that adds holds 128 sums, so the register file is split unevenly: launched with 168
+// registers a thread (384 threads, 64512), warps 0..3 keep 40 and warps 4..11 take 232 (the same sum).
+//
+// Products with few tiles and a long sum split K over the CTAs of a cluster (SPLIT): each adds its
+// share of the blocks, writes its tile to its own shared memory, and the cluster's CTAs sum slices
+// of it in rank order through distributed shared memory, so results do not depend on timing.
+// Every wait is bounded (status bit on timeout; copies in flight land before the CTA exits).
+#include <cooperative_groups.h>
+
+#include "fp8.cuh"
+#include "fp8_tile.cuh"
+#include "tcgen05.cuh"
+#include "tma.cuh"
+
+namespace nvfp4moe {
+namespace {
+
+using namespace sm100;
+
+constexpr int TM = 128;              // rows of A per tile (the MMA's M)
+constexpr int TK = FP8_BLOCK;        // K per stage: one scale block, one 128-byte swizzle row
+constexpr int TTHREADS = 384;
+constexpr int ADD_WARPS = 8;
+constexpr int A_STAGE = TM * TK;
+constexpr uint32_t kTimeout = NVFP4MOE_DEV_TIMEOUT;
+
+enum Mode { DENSE = 0, GATEUP = 1, DOWN = 2 };
+
+constexpr int stages_of(int bn) { return bn == 256 ? 4 : 6; }
+constexpr int ring_bytes(int bn) { return stages_of(bn) * (A_STAGE + bn * TK); }
+constexpr int smem_bytes(int bn) { return 1024 + ring_bytes(bn) + (2 * stages_of(bn) + 5) * 8 + 16 + 2 * 2 * TM * 4; }
+constexpr int split_pitch(int bn) { return bn + 4; }  // floats; rows 16 bytes apart in the banks
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(0u)
+      : "memory");
+}
+
+// kind::f8f6f4 instruction descriptor: fp32 accumulator (bits [4,6) = 1), E4M3 A and B (bits
+// [7,10) and [10,13) = 0), both K-major, N >> 3 at bit 17, M >> 4 at bit 24.
+constexpr uint32_t idesc_f8(int M, int N) {
+  return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  uint32_t a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+  lo = __uint_as_float(a);
+  hi = __uint_as_float(b);
+}
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+
+__device__ __forceinline__ void store_32b(void* p, const uint32_t (&r)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Moves registers between the four-warp groups of a block (all four warps of a group call it).
+template <int N>
+__device__ __forceinline__ void reg_give() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_take() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ void add_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+struct Tile {
+  int e;     // matrix of B (expert)
+  int row;   // first row of A
+  int rows;  // rows of the tile that exist
+  int n0;    // first column
+};
+
+// Tile t of the launch.  Dense: bands of 16 row tiles, column tiles outside rows in a band, so
+// the CTAs that run together read few rows of both operands.  Grouped: the list's row tiles (an
+// expert's are neighbours), column tiles inside.
+__device__ __forceinline__ Tile tile_of(const TileParams& p, int t, int bn, bool grouped) {
+  Tile w;
+  if (grouped) {
+    const int m = t / p.n_nt;
+    const int4 q = __ldg(p.tiles + 1 + m);
+    w.e = q.x, w.row = q.y, w.rows = q.z, w.n0 = (t - m * p.n_nt) * bn;
+  } else {
+    constexpr int BAND = 16;
+    const int band = t / (BAND * p.n_nt), in = t - band * BAND * p.n_nt;
+    const int high = min(BAND, p.n_mt - band * BAND);
+    const int n = in / high;
+    w.e = 0;
+    w.row = (band * BAND + in - n * high) * TM;
+    w.rows = min(TM, p.M - w.row);
+    w.n0 = n * bn;
+  }
+  return w;
+}
+
+template <int MODE, int BN, bool SPLIT>
+__global__ void __launch_bounds__(TTHREADS, 1)
+fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const TileParams p) {
+  constexpr int STAGES = stages_of(BN);
+  constexpr int B_STAGE = BN * TK;
+  constexpr int HALF = BN / 2;          // columns an adding warp holds
+  constexpr bool GROUPED = MODE != DENSE;
+  static_assert(MODE != GATEUP || BN == 256, "a gate/up tile is one 128-column block of each");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_shared_1024(smem_raw);
+  uint8_t* sA = smem;
+  uint8_t* sB = sA + STAGES * A_STAGE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring_bytes(BN));
+  uint64_t* empty = full + STAGES;
+  uint64_t* acc_full = empty + STAGES;  // [2]
+  uint64_t* acc_empty = acc_full + 2;   // [2]
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  uint32_t* s_amax = reinterpret_cast<uint32_t*>(tmem_holder + 4);  // [2][2][128]: tile parity, half, row
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], ADD_WARPS);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, 2 * BN);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&tmA);
+    prefetch_tensormap(&tmB);
+  }
+  griddep_wait();  // the operands may come from the launch before
+  griddep_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  auto abort_now = [&]() {
+    *abort_flag = 1;
+    atomicOr(p.status, kTimeout);
+  };
+
+  const int ranks = SPLIT ? p.split : 1;
+  const int rank = SPLIT ? int(blockIdx.x) % ranks : 0;
+  const int kb0 = int(int64_t(p.nkb) * rank / ranks), kb1 = int(int64_t(p.nkb) * (rank + 1) / ranks);
+  const int n_tiles = (GROUPED ? p.tiles[0].x : p.n_mt) * p.n_nt;
+  const int t_first = int(blockIdx.x) / ranks, t_step = int(gridDim.x) / ranks;
+
+  if (warp < 4) {
+    reg_give<40>();
+    if (warp == 0 && elect_one()) {
+      uint32_t it = 0;
+      for (int t = t_first; t < n_tiles && !*abort_flag; t += t_step) {
+        const Tile w = tile_of(p, t, BN, GROUPED);
+        const int boxes = (w.rows + p.a_box - 1) / p.a_box;
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const int s = it % STAGES;
+          if (!mbar_wait(&empty[s], ((it / STAGES) & 1) ^ 1)) {
+            abort_now();
+            break;
+          }
+          mbar_arrive_expect_tx(&full[s], boxes * p.a_box * TK + B_STAGE);
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d(sA + s * A_STAGE + b * p.a_box * TK, &tmA, kb * TK, w.row + b * p.a_box, &full[s]);
+          if constexpr (MODE == GATEUP) {
+            tma_load_3d(sB + s * B_STAGE, &tmB, kb * TK, w.n0 / 2, 2 * w.e, &full[s]);
+            tma_load_3d(sB + s * B_STAGE + TM * TK, &tmB, kb * TK, w.n0 / 2, 2 * w.e + 1, &full[s]);
+          } else {
+            tma_load_3d(sB + s * B_STAGE, &tmB, kb * TK, w.n0, w.e, &full[s]);
+          }
+        }
+      }
+      if (*abort_flag)
+        for (uint32_t back = 0; back < STAGES && back < it; ++back) {
+          const uint32_t j = it - 1 - back;
+          mbar_wait(&full[j % STAGES], (j / STAGES) & 1, 1u << 16);
+        }
+    } else if (warp == 1 && elect_one()) {
+      constexpr uint32_t idesc = idesc_f8(TM, BN);
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = t_first; t < n_tiles && ok && !*abort_flag; t += t_step) {
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const int s = it % STAGES;
+          const uint32_t ab = it & 1;
+          if (!mbar_wait(&acc_empty[ab], ((it >> 1) & 1) ^ 1) || !mbar_wait(&full[s], (it / STAGES) & 1)) {
+            abort_now();
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t a_d = desc_kmajor_sw128(sA + s * A_STAGE);
+          const uint64_t b_d = desc_kmajor_sw128(sB + s * B_STAGE);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)  // K = 32 per MMA: 32 bytes = 2 descriptor units
+            tc_mma_f8(tmem + ab * BN, a_d + 2 * j, b_d + 2 * j, idesc, j != 0 ? 1u : 0u);
+          tc_commit(&empty[s]);
+          tc_commit(&acc_full[ab]);
+        }
+      }
+      tc_commit(drain);
+      mbar_wait(drain, 0, 1u << 20);
+    }
+  } else {
+    reg_take<232>();
+    const int q = warp & 3;               // the TMEM lane quarter this warp may read
+    const int half = (warp - 4) >> 2;     // its half of the columns
+    const uint32_t trow = tmem + (uint32_t(q * 32) << 16);
+    // the two 32-column runs a step reads: gate and up columns are BN / 2 apart in a gate/up tile
+    auto column = [&](int c) -> uint32_t {
+      if constexpr (MODE == GATEUP) return uint32_t(c < HALF / 2 ? half * (HALF / 2) + c : TM + half * (HALF / 2) + c - HALF / 2);
+      else return uint32_t(half * HALF + c);
+    };
+    constexpr int NS = MODE == GATEUP ? 2 : 1;  // scales of B a warp uses
+    uint32_t it = 0;
+    int done = 0;
+    for (int t = t_first; t < n_tiles && !*abort_flag; t += t_step, ++done) {
+      const Tile w = tile_of(p, t, BN, GROUPED);
+      const int r = q * 32 + lane;
+      const bool live = q * 32 < w.rows;  // the same for the whole warp
+      const float* sa = p.sa + int64_t(w.row + min(r, w.rows - 1)) * p.lda_s;
+      const float* sb[NS];
+      if constexpr (MODE == GATEUP) {
+        sb[0] = p.sb + 2 * w.e * p.sb_e + (w.n0 / 256) * p.ldb_s;
+        sb[1] = sb[0] + p.sb_e;
+      } else {
+        const int nb = min(w.n0 / TK + (BN == 256 ? half : 0), p.nsb - 1);
+        sb[0] = p.sb + w.e * p.sb_e + nb * p.ldb_s;
+      }
+      uint64_t acc[HALF / 2];
+#pragma unroll
+      for (int i = 0; i < HALF / 2; ++i) acc[i] = 0ull;
+      float next[4][NS];  // the scales of the next four blocks
+      auto fetch = [&](int kb) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = min(kb + j, kb1 - 1);
+          const float a = __ldg(sa + k);
+#pragma unroll
+          for (int i = 0; i < NS; ++i) next[j][i] = a * __ldg(sb[i] + k);
+        }
+      };
+      if (kb0 < kb1) fetch(kb0);
+      bool ok = true;
+      for (int kb = kb0; kb < kb1 && ok; kb += 4) {
+        float sc[4][NS];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < NS; ++i) sc[j][i] = next[j][i];
+        fetch(min(kb + 4, kb1 - 1));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (kb + j >= kb1 || !ok) break;
+          const uint32_t ab = it & 1;
+          if (!mbar_wait(&acc_full[ab], (it >> 1) & 1)) {
+            abort_now();
+            ok = false;
+            break;
+          }
+          ++it;
+          tc_fence_after();
+          if (live) {
+#pragma unroll
+            for (int c = 0; c < HALF; c += 32) {
+              uint32_t v[32];
+              tmem_ld_32x32b_x32(trow + ab * BN + column(c), v);
+              tmem_ld_wait();
+              const uint32_t s1 = __float_as_uint(sc[j][NS == 2 && c >= HALF / 2 ? 1 : 0]);
+              const uint64_t s2 = pack2(s1, s1);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) fma2(acc[c / 2 + i], pack2(v[2 * i], v[2 * i + 1]), s2);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[ab]);
+        }
+      }
+      if (!ok) break;
+
+      if constexpr (SPLIT) {
+        // this rank's share, by row, over the idle ring (every stage of it has been consumed)
+        if (live) {
+          float* dst = reinterpret_cast<float*>(smem) + r * split_pitch(BN) + half * HALF;
+#pragma unroll
+          for (int i = 0; i < HALF / 2; i += 2) {
+            float4 f;
+            unpack2(acc[i], f.x, f.y);
+            unpack2(acc[i + 1], f.z, f.w);
+            *reinterpret_cast<float4*>(dst + 2 * i) = f;
+          }
+        }
+      } else if constexpr (MODE == GATEUP) {
+        // h = silu(g) * u, its row's maximum over the 128 columns, then its codes
+        const int i0 = w.n0 / 2;
+        float h[HALF / 2];
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < HALF / 4; ++i) {
+          float g[2], u[2];
+          unpack2(acc[i], g[0], g[1]);
+          unpack2(acc[HALF / 4 + i], u[0], u[1]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            h[2 * i + j] = __fdividef(g[j], 1.0f + __expf(-g[j])) * u[j];
+            m = max(m, abs_bits(h[2 * i + j]));
+          }
+        }
+        uint32_t* sm = s_amax + (done & 1) * 2 * TM;  // two tiles' worth: the barrier below orders reuse
+        sm[half * TM + r] = m;
+        add_barrier();
+        m = max(m, sm[(half ^ 1) * TM + r]);
+        const Fp8Scale f = fp8_scale(m);
+        if (r < w.rows) {
+          const int64_t row = w.row + r;
+          if (half == 0) p.h_scale[row * p.ldh_s + i0 / TK] = f.scale;
+          uint8_t* dst = p.h_codes + row * p.ldh + i0 + half * (HALF / 2);
+#pragma unroll
+          for (int c = 0; c < HALF / 2; c += 16) {
+            if (i0 + half * (HALF / 2) + c < p.I) {  // I is a multiple of 16
+              uint4 o;
+              o.x = fp8_encode4(h + c, f);
+              o.y = fp8_encode4(h + c + 4, f);
+              o.z = fp8_encode4(h + c + 8, f);
+              o.w = fp8_encode4(h + c + 12, f);
+              *reinterpret_cast<uint4*>(dst + c) = o;
+            }
+          }
+        }
+      } else {
+        if (r < w.rows) {
+          const int n = w.n0 + half * HALF;
+          const int64_t at = int64_t(w.row + r) * p.ldd + n;
+          if (p.d_f32) {
+            float* d = static_cast<float*>(p.D) + at;
+#pragma unroll
+            for (int c = 0; c < HALF; c += 8) {
+              float f[8];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) unpack2(acc[c / 2 + i], f[2 * i], f[2 * i + 1]);
+              if (p.d_vec && n + c + 8 <= p.N) {
+                uint32_t o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(f[i]);
+                store_32b(d + c, o);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (n + c + i < p.N) d[c + i] = f[i];
+              }
+            }
+          } else {
+            __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.D) + at;
+#pragma unroll
+            for (int c = 0; c < HALF; c += 16) {
+              uint32_t o[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                float lo, hi;
+                unpack2(acc[c / 2 + i], lo, hi);
+                o[i] = bf16x2(lo, hi);
+              }
+              if (p.d_vec && n + c + 16 <= p.N) {
+                store_32b(d + c, o);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  if (n + c + i < p.N) d[c + i] = __ushort_as_bfloat16(static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1))));
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 2 * BN);
+
+  if constexpr (SPLIT) {
+    // Every CTA of the cluster runs one tile (the grid is tiles * ranks), reaches both barriers on
+    // every path, and sums columns [rank * BN / ranks, +BN / ranks) over the ranks in order.
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    const Tile w = tile_of(p, t_first, BN, GROUPED);
+    const int width = BN / ranks, c0 = rank * width;  // a multiple of 16: ranks is at most 8
+    const int per_row = width / 4;
+    float* mine = reinterpret_cast<float*>(smem);
+    for (int i = threadIdx.x; i < w.rows * per_row; i += TTHREADS) {
+      const int r = i / per_row, c = c0 + (i - r * per_row) * 4;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < ranks; ++k) {
+        const float4 x = *reinterpret_cast<const float4*>(cluster.map_shared_rank(mine, k) + r * split_pitch(BN) + c);
+        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+      }
+      const int n = w.n0 + c;
+      const int64_t at = int64_t(w.row + r) * p.ldd + n;
+      if (p.d_f32) {
+        float* d = static_cast<float*>(p.D) + at;
+        if (p.d_vec && n + 4 <= p.N) {
+          *reinterpret_cast<float4*>(d) = v;
+        } else {
+          const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (n + j < p.N) d[j] = f[j];
+        }
+      } else {
+        __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.D) + at;
+        const uint32_t o[2] = {bf16x2(v.x, v.y), bf16x2(v.z, v.w)};
+        if (p.d_vec && n + 4 <= p.N) {
+          *reinterpret_cast<uint2*>(d) = make_uint2(o[0], o[1]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (n + j < p.N) d[j] = __ushort_as_bfloat16(static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1))));
+        }
+      }
+    }
+    cluster.sync();  // no CTA leaves while another still reads its shared memory
+  }
+}
+
+// [mats][rows][K] bytes, rows `pitch` apart and matrices `mat_pitch`; box 128 bytes x box_rows,
+// 128-byte swizzle.  Rows and bytes past the ends read as zero.
+nvfp4moe_status make_map(CUtensorMap* map, const void* base, int64_t K, int64_t rows, int64_t mats, int64_t pitch,
+                         int64_t mat_pitch, int box_rows, bool three) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return fail(NVFP4MOE_CUDA_ERROR, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint64_t dims[3] = {cuuint64_t(K), cuuint64_t(rows), cuuint64_t(mats)};
+  const cuuint64_t strides[2] = {cuuint64_t(pitch), cuuint64_t(mat_pitch)};
+  const cuuint32_t box[3] = {cuuint32_t(TK), cuuint32_t(box_rows), 1u};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, three ? 3 : 2, const_cast<void*>(base), dims, strides, box,
+                        estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(NVFP4MOE_CUDA_ERROR, "cuTensorMapEncodeTiled failed (%d)", int(r));
+  return NVFP4MOE_OK;
+}
+
+template <int MODE, int BN, bool SPLIT>
+cudaError_t launch_tiles(const CUtensorMap& a, const CUtensorMap& b, const TileParams& p, int grid, cudaStream_t s) {
+  constexpr auto kern = fp8_tile_kernel<MODE, BN, SPLIT>;
+  cudaError_t e = set_smem_limit_once<kern>(smem_bytes(BN));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(TTHREADS);
+  cfg.dynamicSmemBytes = smem_bytes(BN);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  if (SPLIT) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = MODE == DENSE ? 0 : 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, b, p);
+}
+
+}  // namespace
+
+// How a dense product is run: the column width of a tile and the K split.  The estimate is rounds
+// of resident CTAs times the blocks a CTA runs, at the cost of one block: a tile of 256 columns
+// takes 1.7 times one of 128 (its B bytes double, its A bytes do not), and a split adds the
+// exchange of the partial tiles, about three blocks' time.
+DensePlan fp8_dense_plan(int64_t M, int64_t N, int64_t K) {
+  const int sms = num_sms();
+  const int nkb = int(fp8_blocks(K));
+  DensePlan best{256, 1};
+  double least = 1e300;
+  for (int bn : {256, 128})
+    for (int split : {1, 2, 4, 8}) {
+      if (split > nkb) continue;
+      const double tiles = double((M + TM - 1) / TM) * double((N + bn - 1) / bn);
+      const double rounds = split == 1 ? double(int64_t((tiles + sms - 1) / sms)) : double(int64_t((tiles * split + sms - 1) / sms));
+      const double cost = rounds * (((nkb + split - 1) / split) * (bn == 256 ? 1.7 : 1.0) + (split > 1 ? 4.0 : 1.0));
+      if (cost < least * 0.999) {
+        least = cost;
+        best = DensePlan{bn, split};
+      }
+    }
+  return best;
+}
+
+nvfp4moe_status launch_fp8_dense(const uint8_t* A, int64_t lda, const float* A_scale, int64_t lda_s, const uint8_t* B,
+                                 int64_t ldb, const float* B_scale, int64_t ldb_s, int64_t M, int64_t N, int64_t K,
+                                 void* D, int64_t ldd, int d_f32, cudaStream_t s) {
+  const DensePlan plan = fp8_dense_plan(M, N, K);
+  TileParams p{};
+  p.M = int(M), p.N = int(N), p.nkb = int(fp8_blocks(K)), p.nsb = int(fp8_blocks(N));
+  p.n_mt = int((M + TM - 1) / TM), p.n_nt = int((N + plan.bn - 1) / plan.bn);
+  p.a_box = M <= 96 ? 32 : TM;  // short products load only the rows' 32-row groups that exist
+  p.sa = A_scale, p.lda_s = lda_s, p.sb = B_scale, p.ldb_s = ldb_s, p.sb_e = 0;
+  p.D = D, p.ldd = ldd, p.d_f32 = d_f32;
+  const int64_t elt = d_f32 ? 4 : 2;
+  p.d_vec = reinterpret_cast<uintptr_t>(D) % 32 == 0 && ldd * elt % 32 == 0;
+  p.split = plan.split;
+  p.status = device_status_ptr();
+  if (!p.status) return fail(NVFP4MOE_CUDA_ERROR, "device status word unavailable");
+  CUtensorMap am, bm;
+  nvfp4moe_status st = make_map(&am, A, K, M, 1, lda, lda * M, p.a_box, false);
+  if (st == NVFP4MOE_OK) st = make_map(&bm, B, K, N, 1, ldb, ldb * N, plan.bn, true);
+  if (st != NVFP4MOE_OK) return st;
+  const int64_t tiles = int64_t(p.n_mt) * p.n_nt;
+  const int grid = plan.split > 1 ? int(tiles * plan.split) : int(tiles < num_sms() ? tiles : num_sms());
+  cudaError_t e;
+  if (plan.bn == 256)
+    e = plan.split > 1 ? launch_tiles<DENSE, 256, true>(am, bm, p, grid, s) : launch_tiles<DENSE, 256, false>(am, bm, p, grid, s);
+  else
+    e = plan.split > 1 ? launch_tiles<DENSE, 128, true>(am, bm, p, grid, s) : launch_tiles<DENSE, 128, false>(am, bm, p, grid, s);
+  if (e != cudaSuccess) return fail(NVFP4MOE_CUDA_ERROR, "fp8_gemm: %s", cudaGetErrorString(e));
+  return check_launch("fp8_gemm");
+}
+
+nvfp4moe_status launch_fp8_grouped(const GroupedArgs& g, cudaStream_t s) {
+  uint32_t* status = device_status_ptr();
+  if (!status) return fail(NVFP4MOE_CUDA_ERROR, "device status word unavailable");
+  const int nI = int(fp8_blocks(g.I)), nH = int(fp8_blocks(g.H));
+  CUtensorMap xm, w13, hm, w2;
+  nvfp4moe_status st = make_map(&xm, g.x_codes, g.H, g.rows, 1, g.H, int64_t(g.H) * g.rows, 32, false);
+  if (st == NVFP4MOE_OK)
+    st = make_map(&w13, g.w13_codes, g.H, g.I, 2 * int64_t(g.E), g.H, int64_t(g.I) * g.H, TM, true);
+  if (st == NVFP4MOE_OK) st = make_map(&hm, g.h_codes, g.I, g.rows, 1, g.I, int64_t(g.I) * g.rows, 32, false);
+  if (st == NVFP4MOE_OK) st = make_map(&w2, g.w2_codes, g.I, g.H, g.E, g.I, int64_t(g.I) * g.H, 256, true);
+  if (st != NVFP4MOE_OK) return st;
+  TileParams p{};
+  p.a_box = 32;
+  p.tiles = g.tiles;
+  p.status = status;
+  p.split = 1;
+  p.I = g.I;
+  // gate/up: column tile j covers columns [128 j, +128) of gate and of up
+  p.nkb = nH, p.n_nt = nI, p.nsb = nI;
+  p.sa = g.x_scale, p.lda_s = nH;
+  p.sb = g.w13_scale, p.ldb_s = nH, p.sb_e = int64_t(nI) * nH;
+  p.h_codes = g.h_codes, p.ldh = g.I, p.h_scale = g.h_scale, p.ldh_s = nI;
+  const int64_t most = int64_t(g.max_row_tiles) * nI;
+  const int grid1 = int(most < num_sms() ? most : num_sms());
+  cudaError_t e = launch_tiles<GATEUP, 256, false>(xm, w13, p, grid1, s);
+  // down: fp32 rows in expert order
+  p.nkb = nI, p.n_nt = int((g.H + 255) / 256), p.nsb = nH, p.N = g.H;
+  p.sa = g.h_scale, p.lda_s = nI;
+  p.sb = g.w2_scale, p.ldb_s = nI, p.sb_e = int64_t(nH) * nI;
+  p.D = g.slots, p.ldd = g.H, p.d_f32 = 1, p.d_vec = 1;
+  const int64_t most2 = int64_t(g.max_row_tiles) * p.n_nt;
+  const int grid2 = int(most2 < num_sms() ? most2 : num_sms());
+  if (e == cudaSuccess) e = launch_tiles<DOWN, 256, false>(hm, w2, p, grid2, s);
+  if (e != cudaSuccess) return fail(NVFP4MOE_CUDA_ERROR, "fp8 grouped products: %s", cudaGetErrorString(e));
+  return check_launch("fp8 grouped products");
+}
+
+}  // namespace nvfp4moe
+
+using namespace nvfp4moe;
+
+extern "C" nvfp4moe_status fp8_gemm(const uint8_t* A, int64_t lda, const float* A_scale, int64_t lda_s,
+                                    const uint8_t* B, int64_t ldb, const float* B_scale, int64_t ldb_s, int64_t M,
+                                    int64_t N, int64_t K, void* D, int64_t ldd, int32_t d_dtype,
+                                    nvfp4moe_stream_t stream) {
+  const char* fn = "fp8_gemm";
+  NVFP4_REQUIRE(d_dtype == NVFP4MOE_DTYPE_BF16 || d_dtype == NVFP4MOE_DTYPE_F32, NVFP4MOE_INVALID_ARG,
+                "%s: d_dtype=%d", fn, d_dtype);
+  NVFP4_REQUIRE(M >= 0 && N >= 0 && K >= 0, NVFP4MOE_INVALID_ARG, "%s: negative size", fn);
+  if (M == 0 || N == 0) return NVFP4MOE_OK;
+  NVFP4_REQUIRE(K >= 1, NVFP4MOE_UNSUPPORTED_SHAPE, "%s: K=0", fn);
+  const int64_t most = int64_t(1) << 30;
+  NVFP4_REQUIRE(M <= most && N <= most && K <= most && ((M + 127) / 128) * ((N + 127) / 128) <= (int64_t(1) << 27),
+                NVFP4MOE_UNSUPPORTED_SHAPE, "%s: M=%lld N=%lld K=%lld", fn, (long long)M, (long long)N, (long long)K);
+  NVFP4_REQUIRE(A && A_scale && B && B_scale && D, NVFP4MOE_INVALID_ARG, "%s: NULL pointer", fn);
+  const int64_t nkb = fp8_blocks(K);
+  NVFP4_REQUIRE(lda >= K && ldb >= K && ldd >= N && lda_s >= nkb && ldb_s >= nkb, NVFP4MOE_INVALID_ARG,
+                "%s: a row pitch below the row's length", fn);
+  NVFP4_REQUIRE(lda % 16 == 0 && ldb % 16 == 0 && aligned16(A) && aligned16(B), NVFP4MOE_UNSUPPORTED_SHAPE,
+                "%s: rows of A and B must start at multiples of 16 bytes", fn);
+  NVFP4_REQUIRE(lda < (int64_t(1) << 40) && ldb < (int64_t(1) << 40), NVFP4MOE_UNSUPPORTED_SHAPE,
+                "%s: a row pitch of 2^40 bytes or more", fn);
+  const int64_t elt = d_dtype == NVFP4MOE_DTYPE_F32 ? 4 : 2;
+  NVFP4_REQUIRE(reinterpret_cast<uintptr_t>(D) % elt == 0, NVFP4MOE_INVALID_ARG, "%s: D is not aligned to its type",
+                fn);
+  return launch_fp8_dense(A, lda, A_scale, lda_s, B, ldb, B_scale, ldb_s, M, N, K, D, ldd,
+                          d_dtype == NVFP4MOE_DTYPE_F32, reinterpret_cast<cudaStream_t>(stream));
+}

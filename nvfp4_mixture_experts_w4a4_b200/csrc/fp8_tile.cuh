@@ -1,0 +1,56 @@
+// Launch interface of the FP8 tile kernel (fp8_tile.cu).
+#pragma once
+
+#include "common.cuh"
+
+namespace nvfp4moe {
+
+struct TileParams {
+  int M, N;                  // dense: rows of A and B; down: N = H
+  int nkb;                   // 128-blocks of K
+  int nsb;                   // 128-blocks of B's rows (of one matrix)
+  int n_mt, n_nt;            // row tiles (dense), column tiles
+  int a_box;                 // rows of one TMA box of A
+  int split;                 // CTAs that share a tile's K
+  const int4* tiles;         // grouped: [0].x row tiles, then {expert, first row, rows, -} each
+  const float* sa;           // scales of A: row pitch lda_s
+  const float* sb;           // scales of B: 128-row block pitch ldb_s, matrix pitch sb_e
+  int64_t lda_s, ldb_s, sb_e;
+  void* D;
+  int64_t ldd;
+  int d_f32, d_vec;
+  uint8_t* h_codes;          // gate/up: h in E4M3, rows of A
+  float* h_scale;
+  int64_t ldh, ldh_s;
+  int I;
+  uint32_t* status;
+};
+
+struct DensePlan {
+  int bn, split;
+};
+DensePlan fp8_dense_plan(int64_t M, int64_t N, int64_t K);
+
+nvfp4moe_status launch_fp8_dense(const uint8_t* A, int64_t lda, const float* A_scale, int64_t lda_s, const uint8_t* B,
+                                 int64_t ldb, const float* B_scale, int64_t ldb_s, int64_t M, int64_t N, int64_t K,
+                                 void* D, int64_t ldd, int d_f32, cudaStream_t s);
+
+// Gate/up (SwiGLU, h in E4M3) then down (fp32 rows) over the rows of x in expert order.
+struct GroupedArgs {
+  int H, I, E;
+  int64_t rows;              // rows of x_codes, h_codes and slots
+  int max_row_tiles;         // an upper bound of tiles[0].x
+  const int4* tiles;
+  const uint8_t* x_codes;    // [rows][H]
+  const float* x_scale;      // [rows][H / 128]
+  const uint8_t* w13_codes;  // [E][2][I][H]
+  const float* w13_scale;    // [E][2][I / 128][H / 128]
+  const uint8_t* w2_codes;   // [E][H][I]
+  const float* w2_scale;     // [E][H / 128][I / 128]
+  uint8_t* h_codes;          // [rows][I]
+  float* h_scale;            // [rows][I / 128]
+  float* slots;              // [rows][H]
+};
+nvfp4moe_status launch_fp8_grouped(const GroupedArgs& g, cudaStream_t s);
+
+}  // namespace nvfp4moe

@@ -12,11 +12,12 @@ import numpy as np
 import torch
 
 from . import _lib as C
-from ._lib import check, lib
+from ._lib import FP8_BLOCKS, FP8_ROWS, check, lib
 
 __all__ = [
     "nvfp4_quantize", "moe_route", "moe_permute", "nvfp4_gemm", "moe_ffn_forward", "codec_convert",
     "device_status", "sf_mma_bytes", "NVFP4Experts", "MoeFFN",
+    "FP8_ROWS", "FP8_BLOCKS", "fp8_quantize", "fp8_gemm", "FP8Experts", "FP8MoeFFN",
 ]
 
 
@@ -479,8 +480,247 @@ class MoeFFN:
         )
 
 
+def _fp8_blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _same_device(*ts):
+    """The CUDA device the tensors share."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("libnvfp4moe takes CUDA tensors only")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    return dev
+
+
+class _on:
+    """Makes the device of a call's tensors current for its launches (free when it is already)."""
+
+    def __init__(self, dev):
+        self.dev, self.back = dev.index, None
+
+    def __enter__(self):
+        now = torch.cuda.current_device()
+        if now != self.dev:
+            self.back = now
+            torch.cuda.set_device(self.dev)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+
+
+def _fp8_codes(t: torch.Tensor, what: str):
+    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise ValueError(f"{what} must be float8_e4m3fn (or its bytes as uint8), got {t.dtype}")
+
+
+def fp8_quantize(x: torch.Tensor, *, tile: int = FP8_ROWS, codes: torch.Tensor | None = None,
+                 scale: torch.Tensor | None = None):
+    """Quantises x ([rows, K] or [batch, rows, K], bf16 or fp32) to E4M3 with one fp32 scale per
+    1 x 128 (FP8_ROWS: activations) or 128 x 128 group (FP8_BLOCKS: weights): scale = amax / 448,
+    code = the E4M3 value nearest to x / scale.
+
+    Returns (codes float8_e4m3fn shaped like x, scale fp32 [batch?, rows or ceil(rows / 128),
+    ceil(K / 128)]).  Rows of the codes it allocates start every multiple of 16 bytes, as fp8_gemm
+    wants them (for other K the codes are a view of wider rows).  codes / scale: the caller's own,
+    with unit stride along K."""
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x must be [rows, K] or [batch, rows, K], got {tuple(x.shape)}")
+    if x.dtype == torch.bfloat16:
+        dt = C.DTYPE_BF16
+    elif x.dtype == torch.float32:
+        dt = C.DTYPE_F32
+    else:
+        raise ValueError("x must be bf16 or fp32")
+    dev = _same_device(x, codes, scale)
+    shape = x.shape
+    rows, K = shape[-2], shape[-1]
+    B = shape[0] if x.dim() == 3 else 1
+    if K > 1 and x.stride(-1) != 1:
+        raise ValueError("x must have unit stride along K")
+    srows = rows if tile == FP8_ROWS else _fp8_blocks(rows)
+    if codes is None:
+        pitch = (K + 15) // 16 * 16
+        codes = torch.empty(*shape[:-1], pitch, dtype=torch.float8_e4m3fn, device=dev)
+        if pitch != K:
+            codes = codes[..., :K]
+    else:
+        _fp8_codes(codes, "codes")
+        if codes.shape != shape or (K > 1 and codes.stride(-1) != 1):
+            raise ValueError(f"codes must be {tuple(shape)} with unit stride along K")
+    if scale is None:
+        scale = torch.empty(*shape[:-2], srows, _fp8_blocks(K), dtype=torch.float32, device=dev)
+    elif (scale.dtype != torch.float32 or scale.shape != (*shape[:-2], srows, _fp8_blocks(K))
+          or (scale.shape[-1] > 1 and scale.stride(-1) != 1)):
+        raise ValueError(f"scale must be fp32 {(*shape[:-2], srows, _fp8_blocks(K))} with unit stride along K")
+    batched = x.dim() == 3
+    with _on(dev):
+        st = lib().fp8_quantize(x.data_ptr(), dt, B, rows, K, x.stride(-2), x.stride(0) if batched else 0, tile,
+                                codes.data_ptr(), codes.stride(-2), codes.stride(0) if batched else 0,
+                                scale.data_ptr(), scale.stride(-2), scale.stride(0) if batched else 0,
+                                torch.cuda.current_stream().cuda_stream)
+    check(st, "fp8_quantize")
+    return codes, scale
+
+
+def fp8_gemm(A: torch.Tensor, A_scale: torch.Tensor, B: torch.Tensor, B_scale: torch.Tensor,
+             out_dtype=torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+    """D = A . B^T for E4M3 A [M, K] with a scale per row and 128 columns (A_scale fp32 [M,
+    ceil(K / 128)]) and B [N, K] with one per 128 x 128 block (B_scale fp32 [ceil(N / 128),
+    ceil(K / 128)]), as fp8_quantize gives them.  D: bf16 or fp32 [M, N].  Rows of A and B start at
+    multiples of 16 bytes; rows of any tensor may be further apart than their length."""
+    _fp8_codes(A, "A")
+    _fp8_codes(B, "B")
+    if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
+        raise ValueError(f"A must be [M, K] and B [N, K], got {tuple(A.shape)} and {tuple(B.shape)}")
+    M, K = A.shape
+    N = B.shape[0]
+    nk = _fp8_blocks(K)
+    if A_scale.dtype != torch.float32 or A_scale.shape != (M, nk):
+        raise ValueError(f"A_scale must be fp32 {(M, nk)}, got {A_scale.dtype} {tuple(A_scale.shape)}")
+    if B_scale.dtype != torch.float32 or B_scale.shape != (_fp8_blocks(N), nk):
+        raise ValueError(f"B_scale must be fp32 {(_fp8_blocks(N), nk)}, got {B_scale.dtype} {tuple(B_scale.shape)}")
+    if out is not None:
+        out_dtype = out.dtype
+        if out.shape != (M, N):
+            raise ValueError(f"out must be {(M, N)}, got {tuple(out.shape)}")
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("D is bf16 or fp32")
+    dev = _same_device(A, A_scale, B, B_scale, out)
+    if out is None:
+        out = torch.empty(M, N, dtype=out_dtype, device=dev)
+    if (K > 1 and (A.stride(1) != 1 or B.stride(1) != 1)) or (N > 1 and out.stride(1) != 1) or \
+            (nk > 1 and (A_scale.stride(1) != 1 or B_scale.stride(1) != 1)):
+        raise ValueError("every tensor must have unit stride along its last axis")
+
+    def pitch(t, n):  # a single row has no pitch: any that the kernels accept
+        return t.stride(0) if t.shape[0] > 1 else n
+
+    wide = (K + 15) // 16 * 16
+    with _on(dev):
+        st = lib().fp8_gemm(A.data_ptr(), pitch(A, wide), A_scale.data_ptr(), pitch(A_scale, nk), B.data_ptr(),
+                            pitch(B, wide), B_scale.data_ptr(), pitch(B_scale, nk), M, N, K, out.data_ptr(),
+                            pitch(out, N), C.DTYPE_F32 if out_dtype == torch.float32 else C.DTYPE_BF16,
+                            torch.cuda.current_stream().cuda_stream)
+    check(st, "fp8_gemm")
+    return out
+
+
+class FP8Experts:
+    """Per-expert FP8 weights: w13_codes E4M3 [E, 2, I, H] (gate, then up) with w13_scale fp32
+    [E, 2, ceil(I / 128), ceil(H / 128)], w2_codes [E, H, I] with w2_scale [E, ceil(H / 128),
+    ceil(I / 128)]: one scale per 128 x 128 block, as checkpoints keep them."""
+
+    def __init__(self, w13_codes, w13_scale, w2_codes, w2_scale):
+        _fp8_codes(w13_codes, "w13_codes")
+        _fp8_codes(w2_codes, "w2_codes")
+        if w13_codes.dim() != 4 or w13_codes.shape[1] != 2:
+            raise ValueError(f"w13_codes must be [E, 2, I, H], got {tuple(w13_codes.shape)}")
+        self.E, _, self.I, self.H = w13_codes.shape
+        nI, nH = _fp8_blocks(self.I), _fp8_blocks(self.H)
+        for name, t, shape in (("w2_codes", w2_codes, (self.E, self.H, self.I)),
+                               ("w13_scale", w13_scale, (self.E, 2, nI, nH)),
+                               ("w2_scale", w2_scale, (self.E, nH, nI))):
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+        if w13_scale.dtype != torch.float32 or w2_scale.dtype != torch.float32:
+            raise ValueError("scales must be fp32")
+        _same_device(w13_codes, w13_scale, w2_codes, w2_scale)
+        self.w13_codes, self.w13_scale = w13_codes.contiguous(), w13_scale.contiguous()
+        self.w2_codes, self.w2_scale = w2_codes.contiguous(), w2_scale.contiguous()
+
+    @classmethod
+    def from_fp8(cls, gate: tuple, up: tuple, down: tuple) -> "FP8Experts":
+        """Weights already in FP8, each (codes, scales): gate and up [E, I, H], down [E, H, I]."""
+        return cls(torch.stack([gate[0].view(torch.uint8), up[0].view(torch.uint8)], 1),
+                   torch.stack([gate[1], up[1]], 1).float(), down[0], down[1].float())
+
+    @classmethod
+    def from_float(cls, w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor) -> "FP8Experts":
+        """Quantises bf16 or fp32 weights [E, I, H] / [E, H, I] (fp8_quantize, FP8_BLOCKS)."""
+        E, I, H = w_gate.shape
+        dev = w_gate.device
+        codes = torch.empty(E, 2, I, H, dtype=torch.float8_e4m3fn, device=dev)
+        scale = torch.empty(E, 2, _fp8_blocks(I), _fp8_blocks(H), dtype=torch.float32, device=dev)
+        for j, w in enumerate((w_gate, w_up)):
+            fp8_quantize(w, tile=FP8_BLOCKS, codes=codes[:, j], scale=scale[:, j])
+        down = torch.empty(E, H, I, dtype=torch.float8_e4m3fn, device=dev)
+        _, s2 = fp8_quantize(w_down, tile=FP8_BLOCKS, codes=down)
+        return cls(codes, scale, down, s2)
+
+
+class FP8MoeFFN:
+    """The routed feed-forward layer on FP8 weights (fp8_moe_ffn_forward) with a cached workspace:
+    x and the intermediate h are quantised per row and 128 columns inside the call, out is bf16."""
+
+    def __init__(self, experts: FP8Experts, top_k: int):
+        self.w = experts
+        self.top_k = top_k
+        self._ws = {}    # size class (bytes) -> buffer
+        self._need = {}  # T -> workspace bytes
+        d = C.Fp8MoeFfnDesc()
+        d.H, d.I, d.E, d.top_k = experts.H, experts.I, experts.E, top_k
+        d.w13_codes, d.w13_scale = experts.w13_codes.data_ptr(), experts.w13_scale.data_ptr()
+        d.w2_codes, d.w2_scale = experts.w2_codes.data_ptr(), experts.w2_scale.data_ptr()
+        self._desc = d
+        self._descs = {}  # T -> descriptor
+
+    def desc(self, T: int) -> C.Fp8MoeFfnDesc:
+        if T not in self._descs:
+            d = C.Fp8MoeFfnDesc()
+            ctypes.pointer(d)[0] = self._desc
+            d.T = T
+            self._descs[T] = d
+        return self._descs[T]
+
+    def workspace(self, T: int) -> torch.Tensor:
+        """The device workspace of a T-token call: pooled by power-of-two size class and never
+        freed, as MoeFFN.workspace; calls on one layer must be ordered (one stream)."""
+        if T not in self._need:
+            need = int(lib().fp8_moe_ffn_workspace_size(ctypes.byref(self.desc(T))))
+            if need == 0 and T > 0:
+                check(C.UNSUPPORTED_SHAPE, "fp8_moe_ffn_workspace_size")
+            self._need[T] = max(need, 16)
+        size_class = max(1 << 20, 1 << (self._need[T] - 1).bit_length())
+        if size_class not in self._ws:
+            self._ws[size_class] = torch.empty(size_class, dtype=torch.uint8, device=self.w.w13_codes.device)
+        return self._ws[size_class]
+
+    def forward(self, x: torch.Tensor, logits: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+        w = self.w
+        if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != w.H:
+            raise ValueError(f"x must be bf16 [T, {w.H}], got {x.dtype} {tuple(x.shape)}")
+        T = x.shape[0]
+        if tuple(logits.shape) != (T, w.E):
+            raise ValueError(f"logits must be [{T}, {w.E}], got {tuple(logits.shape)}")
+        if out is not None and (out.dtype != torch.bfloat16 or tuple(out.shape) != (T, w.H)
+                                or not out.is_contiguous()):
+            raise ValueError(f"out must be a contiguous bf16 [{T}, {w.H}] tensor")
+        dev = _same_device(x, logits, out, w.w13_codes)
+        with _on(dev):
+            x = x.contiguous()
+            logits = logits.to(torch.float32).contiguous()
+            if out is None:
+                out = torch.empty(T, w.H, dtype=torch.bfloat16, device=dev)
+            ws = self.workspace(T)
+            st = lib().fp8_moe_ffn_forward(ctypes.byref(self.desc(T)), x.data_ptr(), logits.data_ptr(),
+                                           out.data_ptr(), ws.data_ptr(), ws.numel(),
+                                           torch.cuda.current_stream().cuda_stream)
+        check(st, "fp8_moe_ffn_forward")
+        return out
+
+    __call__ = forward
+
+
 class GraphedMoeFFN:
-    """The layer for a fixed batch size T, captured once into a CUDA graph over static buffers:
+    """The layer (MoeFFN or FP8MoeFFN) for a fixed batch size T, captured once into a CUDA graph over static buffers:
     a call copies x and logits into the static inputs (device or pinned host tensors), replays
     the graph (the same kernels as an eager call, without the per-call host work of building
     the call and launching each kernel) and returns the static output (overwritten by the next
@@ -493,7 +733,7 @@ class GraphedMoeFFN:
     CPU); the returned `out_host` is valid once the current stream has reached the replay's
     end (e.g. after torch.cuda.current_stream().synchronize())."""
 
-    def __init__(self, layer: MoeFFN, T: int, host_io: bool = False):
+    def __init__(self, layer: MoeFFN | FP8MoeFFN, T: int, host_io: bool = False):
         dev = layer.w.w13_codes.device
         self.layer, self.T, self.host_io = layer, T, host_io
         self.x = torch.zeros(T, layer.w.H, dtype=torch.bfloat16, device=dev)
