@@ -44,27 +44,109 @@ constexpr uint32_t kTimeout = NVFP4MOE_DEV_TIMEOUT;
 
 enum Mode { DENSE = 0, GATEUP = 1, DOWN = 2 };
 
-constexpr int stages_of(int bn) { return bn == 256 ? 4 : 6; }
-constexpr int ring_bytes(int bn) { return stages_of(bn) * (A_STAGE + bn * TK); }
-constexpr int smem_bytes(int bn) { return 1024 + ring_bytes(bn) + (2 * stages_of(bn) + 5) * 8 + 16 + 2 * 2 * TM * 4; }
+constexpr int SC_BLOCKS = 8;                    // blocks of K whose scales are staged at once: 32 bytes of a row
+constexpr int SC_FLOATS = SC_BLOCKS * 2 * TM;   // [block][half][row]
+
+// rows of B a CTA holds per stage, stages, and shared memory
+constexpr int b_rows(int bn, bool pair) { return pair ? bn / 2 : bn; }
+constexpr int stages_of(int bn, bool pair) { return b_rows(bn, pair) == 256 ? 4 : 6; }
+constexpr int ring_bytes(int bn, bool pair) { return stages_of(bn, pair) * (A_STAGE + b_rows(bn, pair) * TK); }
+constexpr int smem_bytes(int bn, bool pair) {
+  return 1024 + ring_bytes(bn, pair) + (2 * stages_of(bn, pair) + 9) * 8 + 16 + 2 * 2 * TM * 4 + 2 * SC_FLOATS * 4;
+}
 constexpr int split_pitch(int bn) { return bn + 4; }  // floats; rows 16 bytes apart in the banks
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
+// Loads into this CTA's shared memory; PAIR: the bytes are counted on a barrier of either CTA of the
+// pair (bar: its shared::cluster address).
+template <bool PAIR>
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                         uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
 }
 
+// The shared::cluster address of rank's copy of a shared variable of this CTA.
+__device__ __forceinline__ uint32_t cluster_address(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Arrivals that say "these TMEM columns have been read".  The reads are complete (tcgen05.wait::ld)
+// and nothing in memory is passed on, so they are relaxed: a release would wait for the thread's
+// outstanding loads of scales, 1700 cycles a block at cluster scope and 200 at CTA scope.
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive_here(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <bool PAIR>
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                           uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}"
-      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(0u)
-      : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, {%5, %5, %5, %5, %5, %5, %5, %5}, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(0u)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(0u)
+        : "memory");
+}
+
+// Arrives on `bar` (PAIR: in both CTAs) once every MMA issued so far by this thread has completed.
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    tc_commit(bar);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void alloc_tmem(uint32_t* dst, uint32_t ncols) {
+  if constexpr (PAIR) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(dst, ncols);
+    tmem_relinquish();
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ void free_tmem(uint32_t taddr, uint32_t ncols) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+  else
+    tmem_dealloc(taddr, ncols);
 }
 
 // kind::f8f6f4 instruction descriptor: fp32 accumulator (bits [4,6) = 1), E4M3 A and B (bits
@@ -73,19 +155,16 @@ constexpr uint32_t idesc_f8(int M, int N) {
   return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
 
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
-  return v;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-  uint32_t a, b;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
-  lo = __uint_as_float(a);
-  hi = __uint_as_float(b);
-}
-__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+// tcgen05.wait::ld that the registers of the load pass through, so that no use of them can be moved
+// before it while other loads are in flight.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 
 __device__ __forceinline__ void store_32b(void* p, const uint32_t (&r)[8]) {
@@ -122,6 +201,7 @@ struct Tile {
 // Tile t of the launch.  Dense: bands of 16 row tiles, column tiles outside rows in a band, so
 // the CTAs that run together read few rows of both operands.  Grouped: the list's row tiles (an
 // expert's are neighbours), column tiles inside.
+template <bool PAIR>
 __device__ __forceinline__ Tile tile_of(const TileParams& p, int t, int bn, bool grouped) {
   Tile w;
   if (grouped) {
@@ -129,23 +209,26 @@ __device__ __forceinline__ Tile tile_of(const TileParams& p, int t, int bn, bool
     const int4 q = __ldg(p.tiles + 1 + m);
     w.e = q.x, w.row = q.y, w.rows = q.z, w.n0 = (t - m * p.n_nt) * bn;
   } else {
-    constexpr int BAND = 16;
+    constexpr int BAND = PAIR ? 8 : 16;
     const int band = t / (BAND * p.n_nt), in = t - band * BAND * p.n_nt;
     const int high = min(BAND, p.n_mt - band * BAND);
     const int n = in / high;
     w.e = 0;
-    w.row = (band * BAND + in - n * high) * TM;
-    w.rows = min(TM, p.M - w.row);
+    constexpr int high_rows = PAIR ? 2 * TM : TM;
+    w.row = (band * BAND + in - n * high) * high_rows;
+    w.rows = min(high_rows, p.M - w.row);
     w.n0 = n * bn;
   }
   return w;
 }
 
-template <int MODE, int BN, bool SPLIT>
+template <int MODE, int BN, bool SPLIT, bool PAIR>
 __global__ void __launch_bounds__(TTHREADS, 1)
 fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const TileParams p) {
-  constexpr int STAGES = stages_of(BN);
-  constexpr int B_STAGE = BN * TK;
+  constexpr int STAGES = stages_of(BN, PAIR);
+  constexpr int B_ROWS = b_rows(BN, PAIR);
+  constexpr int B_STAGE = B_ROWS * TK;
+  static_assert(!PAIR || (BN == 256 && !SPLIT), "a pair runs 256 x 256 tiles, whole sums");
   constexpr int HALF = BN / 2;          // columns an adding warp holds
   constexpr bool GROUPED = MODE != DENSE;
   static_assert(MODE != GATEUP || BN == 256, "a gate/up tile is one 128-column block of each");
@@ -153,14 +236,17 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   uint8_t* smem = align_shared_1024(smem_raw);
   uint8_t* sA = smem;
   uint8_t* sB = sA + STAGES * A_STAGE;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring_bytes(BN));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring_bytes(BN, PAIR));
   uint64_t* empty = full + STAGES;
   uint64_t* acc_full = empty + STAGES;  // [2]
   uint64_t* acc_empty = acc_full + 2;   // [2]
-  uint64_t* drain = acc_empty + 2;
+  uint64_t* sc_full = acc_empty + 2;    // [2]
+  uint64_t* sc_empty = sc_full + 2;     // [2]
+  uint64_t* drain = sc_empty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   uint32_t* s_amax = reinterpret_cast<uint32_t*>(tmem_holder + 4);  // [2][2][128]: tile parity, half, row
+  float* s_scale = reinterpret_cast<float*>(s_amax + 4 * TM);       // [2][SC_BLOCKS][2][128]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -170,16 +256,17 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], ADD_WARPS);
+      mbar_init(&acc_empty[b], PAIR ? 2 * ADD_WARPS : ADD_WARPS);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sc_full[b], 64);
+      mbar_init(&sc_empty[b], ADD_WARPS);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
     mbar_fence_init();
   }
-  if (warp == 1) {
-    tmem_alloc(tmem_holder, 2 * BN);
-    tmem_relinquish();
-  }
+  if (warp == 1) alloc_tmem<PAIR>(tmem_holder, 2 * BN);
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tmA);
     prefetch_tensormap(&tmB);
@@ -188,6 +275,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   griddep_launch_dependents();
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_barrier();  // both CTAs' barriers exist
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   auto abort_now = [&]() {
@@ -197,41 +285,51 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 
   const int ranks = SPLIT ? p.split : 1;
   const int rank = SPLIT ? int(blockIdx.x) % ranks : 0;
+  const int side = PAIR ? int(cluster_rank()) : 0;  // this CTA's half of the rows of A and of B
   const int kb0 = int(int64_t(p.nkb) * rank / ranks), kb1 = int(int64_t(p.nkb) * (rank + 1) / ranks);
   const int n_tiles = (GROUPED ? p.tiles[0].x : p.n_mt) * p.n_nt;
-  const int t_first = int(blockIdx.x) / ranks, t_step = int(gridDim.x) / ranks;
+  constexpr int CTAS = PAIR ? 2 : 1;
+  const int t_first = int(blockIdx.x) / (ranks * CTAS), t_step = int(gridDim.x) / (ranks * CTAS);
+  auto rows_of = [&](const Tile& w, int sd) { return max(0, min(TM, w.rows - sd * TM)); };
 
   if (warp < 4) {
     reg_give<40>();
     if (warp == 0 && elect_one()) {
       uint32_t it = 0;
       for (int t = t_first; t < n_tiles && !*abort_flag; t += t_step) {
-        const Tile w = tile_of(p, t, BN, GROUPED);
-        const int boxes = (w.rows + p.a_box - 1) / p.a_box;
+        const Tile w = tile_of<PAIR>(p, t, BN, GROUPED);
+        const int boxes = (rows_of(w, side) + p.a_box - 1) / p.a_box;
+        const int all_boxes = PAIR ? boxes + (rows_of(w, side ^ 1) + p.a_box - 1) / p.a_box : boxes;
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const int s = it % STAGES;
           if (!mbar_wait(&empty[s], ((it / STAGES) & 1) ^ 1)) {
             abort_now();
             break;
           }
-          mbar_arrive_expect_tx(&full[s], boxes * p.a_box * TK + B_STAGE);
+          // a pair's bytes are counted by the first CTA, whose MMA reads both halves
+          const uint32_t bar = PAIR ? cluster_address(&full[s], 0) : smem_u32(&full[s]);
+          if (side == 0) mbar_arrive_expect_tx(&full[s], all_boxes * p.a_box * TK + CTAS * B_STAGE);
           for (int b = 0; b < boxes; ++b)
-            tma_load_2d(sA + s * A_STAGE + b * p.a_box * TK, &tmA, kb * TK, w.row + b * p.a_box, &full[s]);
-          if constexpr (MODE == GATEUP) {
-            tma_load_3d(sB + s * B_STAGE, &tmB, kb * TK, w.n0 / 2, 2 * w.e, &full[s]);
-            tma_load_3d(sB + s * B_STAGE + TM * TK, &tmB, kb * TK, w.n0 / 2, 2 * w.e + 1, &full[s]);
+            load_box<PAIR>(sA + s * A_STAGE + b * p.a_box * TK, &tmA, kb * TK, w.row + side * TM + b * p.a_box, 0, bar);
+          if constexpr (MODE == GATEUP && PAIR) {
+            load_box<PAIR>(sB + s * B_STAGE, &tmB, kb * TK, w.n0 / 2, 2 * w.e + side, bar);
+          } else if constexpr (MODE == GATEUP) {
+            load_box<PAIR>(sB + s * B_STAGE, &tmB, kb * TK, w.n0 / 2, 2 * w.e, bar);
+            load_box<PAIR>(sB + s * B_STAGE + TM * TK, &tmB, kb * TK, w.n0 / 2, 2 * w.e + 1, bar);
           } else {
-            tma_load_3d(sB + s * B_STAGE, &tmB, kb * TK, w.n0, w.e, &full[s]);
+            load_box<PAIR>(sB + s * B_STAGE, &tmB, kb * TK, w.n0 + side * B_ROWS, w.e, bar);
           }
         }
       }
-      if (*abort_flag)
+      // the copies land before the CTA leaves (a pair's are counted by its first CTA, and the second
+      // waits for it at the end)
+      if (*abort_flag && side == 0)
         for (uint32_t back = 0; back < STAGES && back < it; ++back) {
           const uint32_t j = it - 1 - back;
           mbar_wait(&full[j % STAGES], (j / STAGES) & 1, 1u << 16);
         }
-    } else if (warp == 1 && elect_one()) {
-      constexpr uint32_t idesc = idesc_f8(TM, BN);
+    } else if (warp == 1 && side == 0 && elect_one()) {
+      constexpr uint32_t idesc = idesc_f8(PAIR ? 2 * TM : TM, BN);
       uint32_t it = 0;
       bool ok = true;
       for (int t = t_first; t < n_tiles && ok && !*abort_flag; t += t_step) {
@@ -248,89 +346,133 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
           const uint64_t b_d = desc_kmajor_sw128(sB + s * B_STAGE);
 #pragma unroll
           for (int j = 0; j < 4; ++j)  // K = 32 per MMA: 32 bytes = 2 descriptor units
-            tc_mma_f8(tmem + ab * BN, a_d + 2 * j, b_d + 2 * j, idesc, j != 0 ? 1u : 0u);
-          tc_commit(&empty[s]);
-          tc_commit(&acc_full[ab]);
+            tc_mma_f8<PAIR>(tmem + ab * BN, a_d + 2 * j, b_d + 2 * j, idesc, j != 0 ? 1u : 0u);
+          commit<PAIR>(&empty[s]);
+          commit<PAIR>(&acc_full[ab]);
         }
       }
-      tc_commit(drain);
+      commit<PAIR>(drain);
       mbar_wait(drain, 0, 1u << 20);
+    } else if (warp >= 2) {
+      // the products of both scales for SC_BLOCKS blocks at a time: a lane takes rows l and l + 64
+      const int l = (warp - 2) * 32 + lane;
+      uint32_t batch = 0;
+      for (int t = t_first; t < n_tiles && !*abort_flag; t += t_step) {
+        const Tile w = tile_of<PAIR>(p, t, BN, GROUPED);
+        const float* sa[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          sa[i] = p.sa + int64_t(w.row + min(side * TM + l + 64 * i, w.rows - 1)) * p.lda_s;
+        // lanes 0..7 read the first half's scale of B for blocks 0..7, lanes 8..15 the second's
+        const int hb = (lane >> 3) & 1;
+        const float* sb;
+        if constexpr (MODE == GATEUP) sb = p.sb + (2 * w.e + hb) * p.sb_e + (w.n0 / 256) * p.ldb_s;
+        else sb = p.sb + w.e * p.sb_e + min(w.n0 / TK + (BN == 256 ? hb : 0), p.nsb - 1) * p.ldb_s;
+        for (int kb = kb0; kb < kb1; kb += SC_BLOCKS, ++batch) {
+          const int last = kb1 - 1;
+          float a[2][SC_BLOCKS];
+#pragma unroll
+          for (int j = 0; j < SC_BLOCKS; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) a[i][j] = __ldg(sa[i] + min(kb + j, last));
+          const float b = __ldg(sb + min(kb + (lane & 7), last));
+          if (!mbar_wait(&sc_empty[batch & 1], ((batch >> 1) & 1) ^ 1)) {
+            abort_now();
+            break;
+          }
+          float* dst = s_scale + (batch & 1) * SC_FLOATS + l;
+#pragma unroll
+          for (int j = 0; j < SC_BLOCKS; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float bj = __shfl_sync(0xffffffffu, b, h * 8 + j);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) dst[(j * 2 + h) * TM + 64 * i] = a[i][j] * bj;
+            }
+          mbar_arrive(&sc_full[batch & 1]);
+        }
+      }
     }
   } else {
     reg_take<232>();
     const int q = warp & 3;               // the TMEM lane quarter this warp may read
     const int half = (warp - 4) >> 2;     // its half of the columns
     const uint32_t trow = tmem + (uint32_t(q * 32) << 16);
+    const uint32_t release_bar = PAIR ? cluster_address(&acc_empty[0], 0) : 0u;
     // the two 32-column runs a step reads: gate and up columns are BN / 2 apart in a gate/up tile
     auto column = [&](int c) -> uint32_t {
       if constexpr (MODE == GATEUP) return uint32_t(c < HALF / 2 ? half * (HALF / 2) + c : TM + half * (HALF / 2) + c - HALF / 2);
       else return uint32_t(half * HALF + c);
     };
-    constexpr int NS = MODE == GATEUP ? 2 : 1;  // scales of B a warp uses
-    uint32_t it = 0;
+    uint32_t it = 0, batch = 0;
     int done = 0;
     for (int t = t_first; t < n_tiles && !*abort_flag; t += t_step, ++done) {
-      const Tile w = tile_of(p, t, BN, GROUPED);
+      const Tile pair_tile = tile_of<PAIR>(p, t, BN, GROUPED);
+      Tile w = pair_tile;  // this CTA's rows of it
+      w.row += side * TM;
+      w.rows = rows_of(pair_tile, side);
       const int r = q * 32 + lane;
       const bool live = q * 32 < w.rows;  // the same for the whole warp
-      const float* sa = p.sa + int64_t(w.row + min(r, w.rows - 1)) * p.lda_s;
-      const float* sb[NS];
-      if constexpr (MODE == GATEUP) {
-        sb[0] = p.sb + 2 * w.e * p.sb_e + (w.n0 / 256) * p.ldb_s;
-        sb[1] = sb[0] + p.sb_e;
-      } else {
-        const int nb = min(w.n0 / TK + (BN == 256 ? half : 0), p.nsb - 1);
-        sb[0] = p.sb + w.e * p.sb_e + nb * p.ldb_s;
-      }
-      uint64_t acc[HALF / 2];
+      float acc[HALF];
 #pragma unroll
-      for (int i = 0; i < HALF / 2; ++i) acc[i] = 0ull;
-      float next[4][NS];  // the scales of the next four blocks
-      auto fetch = [&](int kb) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = min(kb + j, kb1 - 1);
-          const float a = __ldg(sa + k);
-#pragma unroll
-          for (int i = 0; i < NS; ++i) next[j][i] = a * __ldg(sb[i] + k);
+      for (int i = 0; i < HALF; ++i) acc[i] = 0.0f;
+      bool ok = true;
+      auto sums_ready = [&](uint32_t i) { return mbar_try_wait(&acc_full[i & 1], (i >> 1) & 1); };
+      auto wait_sums = [&](uint32_t i) {
+        if (!mbar_wait(&acc_full[i & 1], (i >> 1) & 1)) {
+          abort_now();
+          ok = false;
         }
       };
-      if (kb0 < kb1) fetch(kb0);
-      bool ok = true;
-      for (int kb = kb0; kb < kb1 && ok; kb += 4) {
-        float sc[4][NS];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < NS; ++i) sc[j][i] = next[j][i];
-        fetch(min(kb + 4, kb1 - 1));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (kb + j >= kb1 || !ok) break;
-          const uint32_t ab = it & 1;
-          if (!mbar_wait(&acc_full[ab], (it >> 1) & 1)) {
-            abort_now();
-            ok = false;
-            break;
+      // The accumulator's columns have been read by this warp (tcgen05.wait::ld is the whole warp's).
+      auto release_sums = [&](uint32_t i) {
+        tc_fence_before();
+        if (lane == 0) {
+          if constexpr (PAIR) arrive_at(release_bar + 8 * (i & 1));
+          else arrive_here(&acc_empty[i & 1]);
+        }
+      };
+      // Chunks of 32 columns, each read and added before the next is read: the two warps of a
+      // scheduler cover each other's reads.  A poll of the next block's barrier takes 250 cycles to
+      // come back, so it is sent before the last chunk's additions.
+      bool ready = false;
+#pragma unroll 1
+      for (int kb = kb0; kb < kb1 && ok; kb += SC_BLOCKS, ++batch) {
+        const int n = min(SC_BLOCKS, kb1 - kb);
+        const float* sc = s_scale + (batch & 1) * SC_FLOATS + (MODE == GATEUP || BN == 128 ? 0 : half * TM) + r;
+        if (!mbar_wait(&sc_full[batch & 1], (batch >> 1) & 1)) {
+          abort_now();
+          ok = false;
+          break;
+        }
+#pragma unroll 1
+        for (int j = 0; j < n; ++j, ++it, sc += 2 * TM) {
+          const float s0 = sc[0], s1 = MODE == GATEUP ? sc[TM] : s0;
+          if (!ready) {
+            wait_sums(it);
+            if (!ok) break;
           }
-          ++it;
           tc_fence_after();
           if (live) {
 #pragma unroll
             for (int c = 0; c < HALF; c += 32) {
               uint32_t v[32];
-              tmem_ld_32x32b_x32(trow + ab * BN + column(c), v);
-              tmem_ld_wait();
-              const uint32_t s1 = __float_as_uint(sc[j][NS == 2 && c >= HALF / 2 ? 1 : 0]);
-              const uint64_t s2 = pack2(s1, s1);
+              tmem_ld_32x32b_x32(trow + (it & 1) * BN + column(c), v);
+              tmem_ld_wait_for(v);
+              if (c + 32 == HALF) {
+                release_sums(it);
+                ready = kb + j + 1 < kb1 && sums_ready(it + 1);
+              }
+              const float x = c >= HALF / 2 ? s1 : s0;
 #pragma unroll
-              for (int i = 0; i < 16; ++i) fma2(acc[c / 2 + i], pack2(v[2 * i], v[2 * i + 1]), s2);
+              for (int i = 0; i < 32; ++i) acc[c + i] = fmaf(__uint_as_float(v[i]), x, acc[c + i]);
             }
+          } else {  // rows past the tile's last: the accumulators only pass through
+            release_sums(it);
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&acc_empty[ab]);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_empty[batch & 1]);
       }
       if (!ok) break;
 
@@ -341,8 +483,8 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
           for (int i = 0; i < HALF / 2; i += 2) {
             float4 f;
-            unpack2(acc[i], f.x, f.y);
-            unpack2(acc[i + 1], f.z, f.w);
+            f.x = acc[2 * i], f.y = acc[2 * i + 1];
+            f.z = acc[2 * i + 2], f.w = acc[2 * i + 3];
             *reinterpret_cast<float4*>(dst + 2 * i) = f;
           }
         }
@@ -354,8 +496,8 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
         for (int i = 0; i < HALF / 4; ++i) {
           float g[2], u[2];
-          unpack2(acc[i], g[0], g[1]);
-          unpack2(acc[HALF / 4 + i], u[0], u[1]);
+          g[0] = acc[2 * i], g[1] = acc[2 * i + 1];
+          u[0] = acc[HALF / 2 + 2 * i], u[1] = acc[HALF / 2 + 2 * i + 1];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             h[2 * i + j] = __fdividef(g[j], 1.0f + __expf(-g[j])) * u[j];
@@ -393,7 +535,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             for (int c = 0; c < HALF; c += 8) {
               float f[8];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) unpack2(acc[c / 2 + i], f[2 * i], f[2 * i + 1]);
+              for (int i = 0; i < 4; ++i) f[2 * i] = acc[c + 2 * i], f[2 * i + 1] = acc[c + 2 * i + 1];
               if (p.d_vec && n + c + 8 <= p.N) {
                 uint32_t o[8];
 #pragma unroll
@@ -413,7 +555,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 float lo, hi;
-                unpack2(acc[c / 2 + i], lo, hi);
+                lo = acc[c + 2 * i], hi = acc[c + 2 * i + 1];
                 o[i] = bf16x2(lo, hi);
               }
               if (p.d_vec && n + c + 16 <= p.N) {
@@ -432,8 +574,10 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 
   tc_fence_before();
   __syncthreads();
+  // a pair leaves together: each CTA's shared memory and barriers are used by the other
+  if constexpr (PAIR) cluster_barrier();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 2 * BN);
+  if (warp == 1) free_tmem<PAIR>(tmem, 2 * BN);
 
   if constexpr (SPLIT) {
     // Every CTA of the cluster runs one tile (the grid is tiles * ranks), reaches both barriers on
@@ -441,7 +585,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
-    const Tile w = tile_of(p, t_first, BN, GROUPED);
+    const Tile w = tile_of<PAIR>(p, t_first, BN, GROUPED);
     const int width = BN / ranks, c0 = rank * width;  // a multiple of 16: ranks is at most 8
     const int per_row = width / 4;
     float* mine = reinterpret_cast<float*>(smem);
@@ -483,42 +627,46 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 // [mats][rows][K] bytes, rows `pitch` apart and matrices `mat_pitch`; box 128 bytes x box_rows,
 // 128-byte swizzle.  Rows and bytes past the ends read as zero.
 nvfp4moe_status make_map(CUtensorMap* map, const void* base, int64_t K, int64_t rows, int64_t mats, int64_t pitch,
-                         int64_t mat_pitch, int box_rows, bool three) {
+                         int64_t mat_pitch, int box_rows) {
   auto fn = tensor_map_encoder();
   if (!fn) return fail(NVFP4MOE_CUDA_ERROR, "cuTensorMapEncodeTiled is unavailable");
   const cuuint64_t dims[3] = {cuuint64_t(K), cuuint64_t(rows), cuuint64_t(mats)};
   const cuuint64_t strides[2] = {cuuint64_t(pitch), cuuint64_t(mat_pitch)};
   const cuuint32_t box[3] = {cuuint32_t(TK), cuuint32_t(box_rows), 1u};
   const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, three ? 3 : 2, const_cast<void*>(base), dims, strides, box,
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
                         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(NVFP4MOE_CUDA_ERROR, "cuTensorMapEncodeTiled failed (%d)", int(r));
   return NVFP4MOE_OK;
 }
 
-template <int MODE, int BN, bool SPLIT>
+template <int MODE, int BN, bool SPLIT, bool PAIR>
 cudaError_t launch_tiles(const CUtensorMap& a, const CUtensorMap& b, const TileParams& p, int grid, cudaStream_t s) {
-  constexpr auto kern = fp8_tile_kernel<MODE, BN, SPLIT>;
-  cudaError_t e = set_smem_limit_once<kern>(smem_bytes(BN));
+  constexpr auto kern = fp8_tile_kernel<MODE, BN, SPLIT, PAIR>;
+  cudaError_t e = set_smem_limit_once<kern>(smem_bytes(BN, PAIR));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(TTHREADS);
-  cfg.dynamicSmemBytes = smem_bytes(BN);
+  cfg.dynamicSmemBytes = smem_bytes(BN, PAIR);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  if (SPLIT) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = p.split;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-  } else {
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = MODE == DENSE ? 0 : 1;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (SPLIT || PAIR) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = PAIR ? 2 : p.split;
+    attr[n].val.clusterDim.y = 1;
+    attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (MODE != DENSE) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
   }
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kern, a, b, p);
 }
 
@@ -531,7 +679,7 @@ cudaError_t launch_tiles(const CUtensorMap& a, const CUtensorMap& b, const TileP
 DensePlan fp8_dense_plan(int64_t M, int64_t N, int64_t K) {
   const int sms = num_sms();
   const int nkb = int(fp8_blocks(K));
-  DensePlan best{256, 1};
+  DensePlan best{256, 1, false};
   double least = 1e300;
   for (int bn : {256, 128})
     for (int split : {1, 2, 4, 8}) {
@@ -541,9 +689,12 @@ DensePlan fp8_dense_plan(int64_t M, int64_t N, int64_t K) {
       const double cost = rounds * (((nkb + split - 1) / split) * (bn == 256 ? 1.7 : 1.0) + (split > 1 ? 4.0 : 1.0));
       if (cost < least * 0.999) {
         least = cost;
-        best = DensePlan{bn, split};
+        best = DensePlan{bn, split, false};
       }
     }
+  const double pairs = double((M + 255) / 256) * double((N + 255) / 256);
+  const double cost = double(int64_t((pairs * 2 + sms - 1) / sms)) * (nkb * 1.2 + 1.0);
+  if (M > 128 && cost < least) best = DensePlan{256, 1, true};
   return best;
 }
 
@@ -553,7 +704,8 @@ nvfp4moe_status launch_fp8_dense(const uint8_t* A, int64_t lda, const float* A_s
   const DensePlan plan = fp8_dense_plan(M, N, K);
   TileParams p{};
   p.M = int(M), p.N = int(N), p.nkb = int(fp8_blocks(K)), p.nsb = int(fp8_blocks(N));
-  p.n_mt = int((M + TM - 1) / TM), p.n_nt = int((N + plan.bn - 1) / plan.bn);
+  const int high = plan.pair ? 2 * TM : TM;
+  p.n_mt = int((M + high - 1) / high), p.n_nt = int((N + plan.bn - 1) / plan.bn);
   p.a_box = M <= 96 ? 32 : TM;  // short products load only the rows' 32-row groups that exist
   p.sa = A_scale, p.lda_s = lda_s, p.sb = B_scale, p.ldb_s = ldb_s, p.sb_e = 0;
   p.D = D, p.ldd = ldd, p.d_f32 = d_f32;
@@ -563,16 +715,22 @@ nvfp4moe_status launch_fp8_dense(const uint8_t* A, int64_t lda, const float* A_s
   p.status = device_status_ptr();
   if (!p.status) return fail(NVFP4MOE_CUDA_ERROR, "device status word unavailable");
   CUtensorMap am, bm;
-  nvfp4moe_status st = make_map(&am, A, K, M, 1, lda, lda * M, p.a_box, false);
-  if (st == NVFP4MOE_OK) st = make_map(&bm, B, K, N, 1, ldb, ldb * N, plan.bn, true);
+  nvfp4moe_status st = make_map(&am, A, K, M, 1, lda, lda, p.a_box);
+  if (st == NVFP4MOE_OK) st = make_map(&bm, B, K, N, 1, ldb, ldb, b_rows(plan.bn, plan.pair));
   if (st != NVFP4MOE_OK) return st;
   const int64_t tiles = int64_t(p.n_mt) * p.n_nt;
-  const int grid = plan.split > 1 ? int(tiles * plan.split) : int(tiles < num_sms() ? tiles : num_sms());
+  const int ctas = plan.pair ? 2 : plan.split;  // of one tile
+  const int resident = num_sms() / ctas;
+  const int grid = plan.split > 1 ? int(tiles * ctas) : int(tiles < resident ? tiles : resident) * ctas;
   cudaError_t e;
-  if (plan.bn == 256)
-    e = plan.split > 1 ? launch_tiles<DENSE, 256, true>(am, bm, p, grid, s) : launch_tiles<DENSE, 256, false>(am, bm, p, grid, s);
+  if (plan.pair)
+    e = launch_tiles<DENSE, 256, false, true>(am, bm, p, grid, s);
+  else if (plan.bn == 256)
+    e = plan.split > 1 ? launch_tiles<DENSE, 256, true, false>(am, bm, p, grid, s)
+                       : launch_tiles<DENSE, 256, false, false>(am, bm, p, grid, s);
   else
-    e = plan.split > 1 ? launch_tiles<DENSE, 128, true>(am, bm, p, grid, s) : launch_tiles<DENSE, 128, false>(am, bm, p, grid, s);
+    e = plan.split > 1 ? launch_tiles<DENSE, 128, true, false>(am, bm, p, grid, s)
+                       : launch_tiles<DENSE, 128, false, false>(am, bm, p, grid, s);
   if (e != cudaSuccess) return fail(NVFP4MOE_CUDA_ERROR, "fp8_gemm: %s", cudaGetErrorString(e));
   return check_launch("fp8_gemm");
 }
@@ -582,11 +740,11 @@ nvfp4moe_status launch_fp8_grouped(const GroupedArgs& g, cudaStream_t s) {
   if (!status) return fail(NVFP4MOE_CUDA_ERROR, "device status word unavailable");
   const int nI = int(fp8_blocks(g.I)), nH = int(fp8_blocks(g.H));
   CUtensorMap xm, w13, hm, w2;
-  nvfp4moe_status st = make_map(&xm, g.x_codes, g.H, g.rows, 1, g.H, int64_t(g.H) * g.rows, 32, false);
+  nvfp4moe_status st = make_map(&xm, g.x_codes, g.H, g.rows, 1, g.H, g.H, 32);
   if (st == NVFP4MOE_OK)
-    st = make_map(&w13, g.w13_codes, g.H, g.I, 2 * int64_t(g.E), g.H, int64_t(g.I) * g.H, TM, true);
-  if (st == NVFP4MOE_OK) st = make_map(&hm, g.h_codes, g.I, g.rows, 1, g.I, int64_t(g.I) * g.rows, 32, false);
-  if (st == NVFP4MOE_OK) st = make_map(&w2, g.w2_codes, g.I, g.H, g.E, g.I, int64_t(g.I) * g.H, 256, true);
+    st = make_map(&w13, g.w13_codes, g.H, g.I, 2 * int64_t(g.E), g.H, int64_t(g.I) * g.H, TM);
+  if (st == NVFP4MOE_OK) st = make_map(&hm, g.h_codes, g.I, g.rows, 1, g.I, g.I, 32);
+  if (st == NVFP4MOE_OK) st = make_map(&w2, g.w2_codes, g.I, g.H, g.E, g.I, int64_t(g.I) * g.H, 256);
   if (st != NVFP4MOE_OK) return st;
   TileParams p{};
   p.a_box = 32;
@@ -601,7 +759,7 @@ nvfp4moe_status launch_fp8_grouped(const GroupedArgs& g, cudaStream_t s) {
   p.h_codes = g.h_codes, p.ldh = g.I, p.h_scale = g.h_scale, p.ldh_s = nI;
   const int64_t most = int64_t(g.max_row_tiles) * nI;
   const int grid1 = int(most < num_sms() ? most : num_sms());
-  cudaError_t e = launch_tiles<GATEUP, 256, false>(xm, w13, p, grid1, s);
+  cudaError_t e = launch_tiles<GATEUP, 256, false, false>(xm, w13, p, grid1, s);
   // down: fp32 rows in expert order
   p.nkb = nI, p.n_nt = int((g.H + 255) / 256), p.nsb = nH, p.N = g.H;
   p.sa = g.h_scale, p.lda_s = nI;
@@ -609,7 +767,7 @@ nvfp4moe_status launch_fp8_grouped(const GroupedArgs& g, cudaStream_t s) {
   p.D = g.slots, p.ldd = g.H, p.d_f32 = 1, p.d_vec = 1;
   const int64_t most2 = int64_t(g.max_row_tiles) * p.n_nt;
   const int grid2 = int(most2 < num_sms() ? most2 : num_sms());
-  if (e == cudaSuccess) e = launch_tiles<DOWN, 256, false>(hm, w2, p, grid2, s);
+  if (e == cudaSuccess) e = launch_tiles<DOWN, 256, false, false>(hm, w2, p, grid2, s);
   if (e != cudaSuccess) return fail(NVFP4MOE_CUDA_ERROR, "fp8 grouped products: %s", cudaGetErrorString(e));
   return check_launch("fp8 grouped products");
 }

@@ -26,8 +26,10 @@ struct TileParams {
   uint32_t* status;
 };
 
+// Columns of a tile, CTAs that split its K, and whether a pair of CTAs runs a tile of 256 rows.
 struct DensePlan {
   int bn, split;
+  bool pair;
 };
 DensePlan fp8_dense_plan(int64_t M, int64_t N, int64_t K);
 
