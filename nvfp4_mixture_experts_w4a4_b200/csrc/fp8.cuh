@@ -21,54 +21,102 @@ inline int64_t fp8_blocks(int64_t n) { return (n + FP8_BLOCK - 1) / FP8_BLOCK; }
 // infinity, so a maximum of these keeps a NaN.
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
-// How a group divides by its scale.  mul scales the element before the division (a power of two, so
-// that residuals of very small groups stay normal numbers), s and inv are the scale times mul and
-// its reciprocal; plain: divide with the IEEE operation (zero, infinite or NaN scales).
+// How a group divides by its scale.  fast: the scale is an ordinary number; inv approximates its
+// reciprocal to an ulp, and lo and hi are the reciprocal less and plus 2^-21 of it.  Otherwise (zero,
+// tiny, infinite or NaN maxima) elements take the slow form.
 struct Fp8Scale {
-  float scale, s, inv, mul;
-  bool plain;
+  float scale, inv, lo, hi;
+  bool fast;
 };
 
 __device__ __forceinline__ Fp8Scale fp8_scale(uint32_t amax_bits) {
   Fp8Scale f;
-  f.scale = __fdiv_rn(__uint_as_float(amax_bits), FP8_MAX);
-  f.mul = f.scale < 0x1p-60f ? 0x1p96f : 1.0f;
-  f.s = f.scale * f.mul;
-  f.inv = __frcp_rn(f.s);
-  f.plain = !(f.scale > 0.0f && f.scale < __uint_as_float(0x7F800000u));
+  const float amax = __uint_as_float(amax_bits);
+  f.fast = amax_bits >= 0x26800000u && amax_bits < 0x7F800000u;  // [2^-50, infinity)
+  if (f.fast) {
+    // rn(amax / 448): one residual step on amax * rn(1 / 448)
+    constexpr float c = 1.0f / FP8_MAX;
+    const float q = amax * c;
+    f.scale = __fmaf_rn(__fmaf_rn(-FP8_MAX, q, amax), c, q);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(f.inv) : "f"(f.scale));
+  } else {
+    f.scale = __fdiv_rn(amax, FP8_MAX);
+    f.inv = 0.0f;
+  }
+  f.lo = f.inv * (1.0f - 0x1p-21f);
+  f.hi = f.inv * (1.0f + 0x1p-21f);
   return f;
 }
 
-// A value on the same side of every E4M3 border as the real quotient x / scale.  q, one Newton
-// step from x * inv, is one of the two fp32 values next to the quotient; where it is not exact
-// (the residual r is not zero) the result is the neighbour towards zero with its last bit set.
-// Borders have four or five significant bits, so the result is never a border unless the quotient is.
-__device__ __forceinline__ float fp8_quotient(float x, const Fp8Scale& f) {
-  const float xm = x * f.mul;
-  const float q0 = xm * f.inv;
-  const float q = __fmaf_rn(__fmaf_rn(-q0, f.s, xm), f.inv, q0);
-  const float r = __fmaf_rn(-q, f.s, xm);
-  uint32_t b = __float_as_uint(q);
-  if (r != 0.0f) {
-    // the quotient is nearer to zero than q when r's sign differs from q's; q = +-0 stays
-    if (int32_t(__float_as_uint(r) ^ b) < 0 && (b & 0x7FFFFFFFu) != 0u) b -= 1u;
-    b |= 1u;
-  }
-  return __uint_as_float(b);
+// A value on the same side of every E4M3 border as the real quotient x / s.  q, one Newton step from
+// x * inv, is one of the two fp32 values next to the quotient; where it is not exact (the residual r
+// is not zero) the result is the neighbour towards zero with its last bit set.  Borders have four or
+// five significant bits, so the result is on one only if the quotient is.  (A quotient that
+// underflows keeps the sign of x and stays below the smallest border.)
+__device__ __forceinline__ float fp8_quotient(float x, float s, float inv) {
+  const float q0 = x * inv;
+  const float q = __fmaf_rn(__fmaf_rn(-q0, s, x), inv, q0);
+  const float r = __fmaf_rn(-q, s, x);
+  const int32_t b = __float_as_int(q);
+  const int32_t odd = (b + ((__float_as_int(r) ^ b) >> 31)) | 1;  // towards zero when r's sign is not q's
+  return r != 0.0f ? __int_as_float(odd) : q;
 }
 
-// Zero scale: every code 0.  Infinite scale: 0 for finite x, NaN for an infinite one.  NaN: NaN.
-__device__ __forceinline__ float fp8_quotient_plain(float x, const Fp8Scale& f) {
-  return f.scale == 0.0f ? 0.0f : __fdiv_rn(x, f.scale);
+// Zero scale: 0.  Infinite: 0 for a finite x, NaN for an infinite one.  NaN: NaN.  Tiny: as above
+// with both sides scaled up by 2^96, so that the residuals are ordinary numbers.
+__device__ __forceinline__ float fp8_quotient_slow(float x, float scale) {
+  if (scale == 0.0f) return 0.0f;
+  if (!(scale < 1.0f)) return __fdiv_rn(x, scale);
+  const float s = scale * 0x1p96f;
+  return fp8_quotient(x * 0x1p96f, s, __frcp_rn(s));
 }
 
-// Four codes, v[0] in the low byte.
+static __device__ __noinline__ uint32_t fp8_encode4_exact(float v0, float v1, float v2, float v3, float scale, float inv,
+                                                         bool fast) {
+  const float v[4] = {v0, v1, v2, v3};
+  float q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q[i] = fast ? fp8_quotient(v[i], scale, inv) : fp8_quotient_slow(v[i], scale);
+  return e4m3x2_from_f32(q[0], q[1]) | (e4m3x2_from_f32(q[2], q[3]) << 16);
+}
+
+// Four codes, v[0] in the low byte.  The real quotients lie between v * lo and v * hi; where both
+// round to the same codes those are the answer (four instructions an element), and where a border
+// lies between (one element in 2^16, and ties) the exact form decides.
 __device__ __forceinline__ uint32_t fp8_encode4(const float* v, const Fp8Scale& f) {
-  if (f.plain)
-    return e4m3x2_from_f32(fp8_quotient_plain(v[0], f), fp8_quotient_plain(v[1], f)) |
-           (e4m3x2_from_f32(fp8_quotient_plain(v[2], f), fp8_quotient_plain(v[3], f)) << 16);
-  return e4m3x2_from_f32(fp8_quotient(v[0], f), fp8_quotient(v[1], f)) |
-         (e4m3x2_from_f32(fp8_quotient(v[2], f), fp8_quotient(v[3], f)) << 16);
+  const uint32_t lo = e4m3x2_from_f32(v[0] * f.lo, v[1] * f.lo) | (e4m3x2_from_f32(v[2] * f.lo, v[3] * f.lo) << 16);
+  const uint32_t hi = e4m3x2_from_f32(v[0] * f.hi, v[1] * f.hi) | (e4m3x2_from_f32(v[2] * f.hi, v[3] * f.hi) << 16);
+  if (lo == hi && f.fast) return lo;
+  return fp8_encode4_exact(v[0], v[1], v[2], v[3], f.scale, f.inv, f.fast);
+}
+
+// The same codes for bf16 elements, without a branch.  With x = mx 2^i, amax = ma 2^j (integers below
+// 256), 448 x / amax differs from a border t 2^k (t odd, below 32) by nothing or by more than 2^-13 of
+// it: |7 mx 2^h - ma t| is 0 or at least 1.  Where it differs, any multiplier within 2^-20 of 1 / scale
+// rounds to the right code.  Where it does not, x / scale lies on the side of the border that the
+// scale's own rounding left it on, the same for the whole group: m is the reciprocal less 2^-21 of
+// it if the scale was rounded up, plus 2^-21 if down; and if the scale is exact, so is the quotient,
+// and a Newton step (n = the reciprocal, else 0) finds it.
+struct Fp8ScaleBf16 {
+  float scale, m, n;
+  bool fast;
+};
+
+__device__ __forceinline__ Fp8ScaleBf16 fp8_scale_bf16(uint32_t amax_bits) {
+  const Fp8Scale f = fp8_scale(amax_bits);
+  const float r = __fmaf_rn(-FP8_MAX, f.scale, __uint_as_float(amax_bits));
+  return Fp8ScaleBf16{f.scale, r > 0.0f ? f.hi : (r < 0.0f ? f.lo : f.inv), r == 0.0f ? f.inv : 0.0f, f.fast};
+}
+
+__device__ __forceinline__ uint32_t fp8_encode4(const float* v, const Fp8ScaleBf16& f) {
+  if (!f.fast) return fp8_encode4_exact(v[0], v[1], v[2], v[3], f.scale, 0.0f, false);
+  float q[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float q0 = v[i] * f.m;
+    q[i] = __fmaf_rn(__fmaf_rn(-q0, f.scale, v[i]), f.n, q0);
+  }
+  return e4m3x2_from_f32(q[0], q[1]) | (e4m3x2_from_f32(q[2], q[3]) << 16);
 }
 
 }  // namespace nvfp4moe

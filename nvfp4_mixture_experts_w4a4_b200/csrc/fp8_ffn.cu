@@ -74,7 +74,7 @@ fp8_place_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict_
   for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const Fp8Scale f = fp8_scale(m);
+  const Fp8ScaleBf16 f = fp8_scale_bf16(m);
   const uint2 out = make_uint2(fp8_encode4(v, f), fp8_encode4(v + 4, f));
   if (!live) return;
   for (int j = 0; j < k; ++j) {

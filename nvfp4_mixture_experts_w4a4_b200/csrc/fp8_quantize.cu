@@ -1,8 +1,8 @@
 // fp8_quantize: bf16 / fp32 -> E4M3 with one fp32 scale per 1 x 128 or 128 x 128 group.
 //
 // Each element is read once and each code written once, so the bound is memory: 3 (bf16) or 5
-// (fp32) bytes an element.  A row group is held by half a warp (bf16: 16 bytes a lane) or a whole
-// one (fp32), its maximum found by shuffles; four steps are loaded before the first is used.  A
+// (fp32) bytes an element.  A row group is held by eight lanes (16 elements each: fewer lanes leave the shuffles,
+// the scale and the addresses to fewer instructions an element), two groups in flight a lane.  A
 // square block is held in the registers of one CTA (64 elements a thread), so it too is read once.
 // Rows whose start, pitch or length does not allow 16-byte loads take scalar ones.
 #include "fp8.cuh"
@@ -19,38 +19,68 @@ struct QuantArgs {
   int64_t lds, s_batch;
 };
 
-template <typename T>
-__device__ __forceinline__ float to_f32(T v) {
-  if constexpr (sizeof(T) == 2) return __bfloat162float(v);
-  else return v;
+// W 32-bit words of elements (two bf16 or one fp32 each), read as they are: n elements exist, the
+// others are zero.  VECTOR: p is aligned to the words' size.
+template <typename T, int W, bool VECTOR>
+__device__ __forceinline__ void load_words(const T* p, int n, uint32_t* u) {
+  constexpr int PER = 4 / sizeof(T);
+  if (VECTOR && n >= W * PER) {
+    if constexpr (W == 4) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+      u[0] = q.x, u[1] = q.y, u[2] = q.z, u[3] = q.w;
+    } else {
+      const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+      u[0] = q.x, u[1] = q.y;
+    }
+  } else if constexpr (PER == 1) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) u[i] = i < n ? __float_as_uint(__ldg(p + i)) : 0u;
+  } else {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      u[i] = 2 * i < n ? __ldg(h + 2 * i) : 0u;
+      if (2 * i + 1 < n) u[i] |= uint32_t(__ldg(h + 2 * i + 1)) << 16;
+    }
+  }
 }
 
-// VEC elements from p (n of them exist); VECTOR: p is aligned to VEC elements.
-template <typename T, int VEC, bool VECTOR>
-__device__ __forceinline__ void load_elements(const T* p, int n, float* v) {
-  if (VECTOR && n >= VEC) {
-    if constexpr (sizeof(T) == 2) {
+// The largest magnitude of the words' elements, as fp32 bits (a NaN stays above everything).
+template <typename T, int W>
+__device__ __forceinline__ uint32_t words_max(const uint32_t* u) {
+  uint32_t m = 0;
+  if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int i = 0; i < VEC / 8; ++i) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-          v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC / 4; ++i) {
-        const float4 u = __ldg(reinterpret_cast<const float4*>(p) + i);
-        v[4 * i] = u.x, v[4 * i + 1] = u.y, v[4 * i + 2] = u.z, v[4 * i + 3] = u.w;
-      }
-    }
+    for (int i = 0; i < W; ++i) m = max(m, u[i] & 0x7FFFFFFFu);
   } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = i < n ? to_f32(p[i]) : 0.0f;
+    for (int i = 0; i < W; ++i) m = __vmaxu2(m, u[i] & 0x7FFF7FFFu);
+    m = max(m << 16, m & 0xFFFF0000u);
   }
+  return m;
+}
+
+// A group's scale as its elements' type uses it.
+template <typename T>
+__device__ __forceinline__ auto scale_for(uint32_t m) {
+  if constexpr (sizeof(T) == 2) return fp8_scale_bf16(m);
+  else return fp8_scale(m);
+}
+
+template <typename T, typename S>
+__device__ __forceinline__ uint32_t encode_words(const uint32_t* u, const S& f) {  // four elements
+  float v[4];
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(u[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  }
+  return fp8_encode4(v, f);
 }
 
 // 4 * W codes to p (n of them exist); ALIGNED: p is aligned to 4 * W bytes.
@@ -68,65 +98,71 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int n, const uint32_t* w
 }
 
 constexpr int kThreads = 256;
+constexpr int kLanes = 8;  // lanes that hold a row group
+constexpr int kBlockThreads = 512;
 
 template <typename T, bool VECTOR>
-__global__ void __launch_bounds__(kThreads) fp8_rows_kernel(QuantArgs a) {
-  constexpr int VEC = 16 / sizeof(T);      // elements a lane: one 16-byte load
-  constexpr int LANES = FP8_BLOCK / VEC;   // lanes a group: 16 (bf16) or 32 (fp32)
-  constexpr int DEPTH = 4;                 // groups in flight a lane
-  const int64_t nb = (a.K + FP8_BLOCK - 1) / FP8_BLOCK;
-  const int64_t groups = a.batch * a.rows * nb;
-  const int sub = threadIdx.x % LANES;
-  const int64_t first = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / LANES;
-  const int64_t step = int64_t(gridDim.x) * (kThreads / LANES);
-  const T* x = static_cast<const T*>(a.x);
-  // the loop's trip count is the same for the lanes of a warp: `first` less the lane's own share
-  const int64_t warp_first = (int64_t(blockIdx.x) * kThreads + (threadIdx.x & ~31)) / LANES;
-  for (int64_t base = 0; warp_first + base < groups; base += DEPTH * step) {
-    float v[DEPTH][VEC];
-    int64_t row[DEPTH];
-    int b[DEPTH];
+__global__ void __launch_bounds__(kThreads, 4) fp8_rows_kernel(QuantArgs a) {
+  constexpr int VEC = 16 / sizeof(T);                  // elements of a 16-byte load
+  constexpr int CHUNKS = FP8_BLOCK / (VEC * kLanes);   // loads a lane and group: 2 (bf16), 4 (fp32)
+  constexpr int DEPTH = 2;                             // groups in flight a lane
+  const int nb = int((a.K + FP8_BLOCK - 1) / FP8_BLOCK);
+  const int64_t groups = a.rows * nb;
+  const int sub = threadIdx.x % kLanes;
+  // this lane's groups: first, first + step, ...; (row, b) is the current one
+  const int64_t first = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / kLanes;
+  const int64_t step = int64_t(gridDim.x) * (kThreads / kLanes);
+  const int64_t step_rows = step / nb;
+  const int step_b = int(step - step_rows * nb);
+  const int K = int(a.K) - sub * VEC;  // elements of a row from this lane's first on
+  for (int64_t bi = blockIdx.y; bi < a.batch; bi += gridDim.y) {
+    const T* x = static_cast<const T*>(a.x) + bi * a.x_batch + sub * VEC;
+    uint8_t* codes = a.codes + bi * a.c_batch + sub * VEC;
+    float* scale = a.scale + bi * a.s_batch;
+    int64_t row = first / nb;
+    int b = int(first - row * nb);
+    // the lanes of a warp take the same turns (its last groups may not exist)
+    for (int64_t left = groups - (first - (threadIdx.x & 31) / kLanes); left > 0; left -= DEPTH * step) {
+      uint32_t u[DEPTH][CHUNKS][4];
+      int64_t rows[DEPTH];
+      int cs[DEPTH];
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) {
-      const int64_t g = first + base + d * step;
-      row[d] = -1;
-      b[d] = 0;
-      if (g < groups) {
-        row[d] = groups <= INT32_MAX ? int64_t(uint32_t(g) / uint32_t(nb)) : g / nb;
-        b[d] = int(g - row[d] * nb);
-        const int64_t bi = a.batch == 1 ? 0 : row[d] / a.rows, r = row[d] - bi * a.rows;
-        const int64_t c = int64_t(b[d]) * FP8_BLOCK + sub * VEC;
-        load_elements<T, VEC, VECTOR>(x + bi * a.x_batch + r * a.ldx + c, int(min(a.K - c, int64_t(VEC))), v[d]);
-      } else {
+      for (int d = 0; d < DEPTH; ++d) {
+        rows[d] = row;
+        cs[d] = row < a.rows ? b * FP8_BLOCK : INT32_MAX / 2;  // past the row's end: nothing is read or written
+        const T* p = x + row * a.ldx + b * FP8_BLOCK;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[d][i] = 0.0f;
+        for (int j = 0; j < CHUNKS; ++j)
+          load_words<T, 4, VECTOR>(p + j * kLanes * VEC, K - cs[d] - j * kLanes * VEC, u[d][j]);
+        row += step_rows, b += step_b;
+        if (b >= nb) b -= nb, ++row;
       }
-    }
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) {
-      uint32_t m = 0;
+      for (int d = 0; d < DEPTH; ++d) {
+        uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) m = max(m, abs_bits(v[d][i]));
+        for (int j = 0; j < CHUNKS; ++j) m = max(m, words_max<T, 4>(u[d][j]));
 #pragma unroll
-      for (int o = LANES / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const Fp8Scale f = fp8_scale(m);
-      if (row[d] >= 0) {
-        const int64_t bi = a.batch == 1 ? 0 : row[d] / a.rows, r = row[d] - bi * a.rows;
-        const int64_t c = int64_t(b[d]) * FP8_BLOCK + sub * VEC;
-        uint32_t w[VEC / 4];
+        for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const auto f = scale_for<T>(m);
+        uint8_t* q = codes + rows[d] * a.ldc + cs[d];
 #pragma unroll
-        for (int i = 0; i < VEC / 4; ++i) w[i] = fp8_encode4(v[d] + 4 * i, f);
-        store_codes<VEC / 4, VECTOR>(a.codes + bi * a.c_batch + r * a.ldc + c, int(min(a.K - c, int64_t(VEC))), w);
-        if (sub == 0) a.scale[bi * a.s_batch + r * a.lds + b[d]] = f.scale;
+        for (int j = 0; j < CHUNKS; ++j) {
+          uint32_t w[VEC / 4];
+#pragma unroll
+          for (int i = 0; i < VEC / 4; ++i) w[i] = encode_words<T>(u[d][j] + i * sizeof(T), f);
+          store_codes<VEC / 4, VECTOR>(q + j * kLanes * VEC, K - cs[d] - j * kLanes * VEC, w);
+        }
+        if (sub == 0 && cs[d] < K) scale[rows[d] * a.lds + cs[d] / FP8_BLOCK] = f.scale;
       }
     }
   }
 }
 
-// One CTA per 128 x 128 block: warp w holds rows w, w + 8, ...; a lane four consecutive columns.
+// One CTA per 128 x 128 block: warp w holds rows w, w + 16, ...; a lane four consecutive columns.
 template <typename T, bool VECTOR>
-__global__ void __launch_bounds__(kThreads) fp8_blocks_kernel(QuantArgs a) {
-  constexpr int WARPS = kThreads / 32, ROWS = FP8_BLOCK / WARPS;
+__global__ void __launch_bounds__(kBlockThreads, 2) fp8_blocks_kernel(QuantArgs a) {
+  constexpr int WARPS = kBlockThreads / 32, ROWS = FP8_BLOCK / WARPS;
   __shared__ uint32_t s_max[WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t nb = (a.K + FP8_BLOCK - 1) / FP8_BLOCK, nr = (a.rows + FP8_BLOCK - 1) / FP8_BLOCK;
@@ -135,42 +171,29 @@ __global__ void __launch_bounds__(kThreads) fp8_blocks_kernel(QuantArgs a) {
   const int64_t c = b * FP8_BLOCK + lane * 4;
   const int n = int(max(int64_t(0), min(a.K - c, int64_t(4))));
   const T* x = static_cast<const T*>(a.x) + bi * a.x_batch + c;
-  float v[ROWS][4];
+  constexpr int W = sizeof(T);  // 32-bit words of four elements
+  uint32_t u[ROWS][W];
+  uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
     const int64_t r = rb * FP8_BLOCK + warp + i * WARPS;
-    const int m = r < a.rows ? n : 0;
-    const T* p = x + r * a.ldx;
-    if (VECTOR && m == 4) {
-      if constexpr (sizeof(T) == 2) {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-        v[i][0] = __uint_as_float(u.x << 16), v[i][1] = __uint_as_float(u.x & 0xFFFF0000u);
-        v[i][2] = __uint_as_float(u.y << 16), v[i][3] = __uint_as_float(u.y & 0xFFFF0000u);
-      } else {
-        load_elements<T, 4, true>(p, 4, v[i]);
-      }
-    } else {
-      load_elements<T, 4, false>(p, m, v[i]);
-    }
+    load_words<T, W, VECTOR>(x + r * a.ldx, r < a.rows ? n : 0, u[i]);
   }
-  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m = max(m, abs_bits(v[i][j]));
+  for (int i = 0; i < ROWS; ++i) m = max(m, words_max<T, W>(u[i]));
   m = __reduce_max_sync(0xffffffffu, m);
   if (lane == 0) s_max[warp] = m;
   __syncthreads();
   m = 0;
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) m = max(m, s_max[w]);
-  const Fp8Scale f = fp8_scale(m);
+  const auto f = scale_for<T>(m);
   if (threadIdx.x == 0) a.scale[bi * a.s_batch + rb * a.lds + b] = f.scale;
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
     const int64_t r = rb * FP8_BLOCK + warp + i * WARPS;
     if (r < a.rows && n > 0) {
-      const uint32_t w = fp8_encode4(v[i], f);
+      const uint32_t w = encode_words<T>(u[i], f);
       store_codes<1, VECTOR>(a.codes + bi * a.c_batch + r * a.ldc + c, n, &w);
     }
   }
@@ -178,10 +201,11 @@ __global__ void __launch_bounds__(kThreads) fp8_blocks_kernel(QuantArgs a) {
 
 template <typename T>
 void launch_rows(const QuantArgs& a, bool vec, cudaStream_t s) {
-  const int64_t per_block = kThreads / (FP8_BLOCK / (16 / int64_t(sizeof(T))));
-  const int64_t want = (a.batch * a.rows * fp8_blocks(a.K) + per_block - 1) / per_block;
+  const int64_t per_block = kThreads / kLanes;
+  const int64_t want = (a.rows * fp8_blocks(a.K) + per_block - 1) / per_block;
   const int64_t most = int64_t(num_sms()) * 8;  // eight CTAs an SM, then a grid-wide stride
-  const dim3 grid(static_cast<unsigned>(want < most ? want : most));
+  const dim3 grid(static_cast<unsigned>(want < most ? want : most),
+                  static_cast<unsigned>(a.batch < 65535 ? a.batch : 65535));
   if (vec) fp8_rows_kernel<T, true><<<grid, kThreads, 0, s>>>(a);
   else fp8_rows_kernel<T, false><<<grid, kThreads, 0, s>>>(a);
 }
@@ -189,8 +213,8 @@ void launch_rows(const QuantArgs& a, bool vec, cudaStream_t s) {
 template <typename T>
 void launch_blocks(const QuantArgs& a, bool vec, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(a.batch * fp8_blocks(a.rows) * fp8_blocks(a.K)));
-  if (vec) fp8_blocks_kernel<T, true><<<grid, kThreads, 0, s>>>(a);
-  else fp8_blocks_kernel<T, false><<<grid, kThreads, 0, s>>>(a);
+  if (vec) fp8_blocks_kernel<T, true><<<grid, kBlockThreads, 0, s>>>(a);
+  else fp8_blocks_kernel<T, false><<<grid, kBlockThreads, 0, s>>>(a);
 }
 
 }  // namespace
@@ -209,8 +233,8 @@ extern "C" nvfp4moe_status fp8_quantize(const void* x, int32_t x_dtype, int64_t 
                 tile);
   NVFP4_REQUIRE(batch >= 0 && rows >= 0 && K >= 0, NVFP4MOE_INVALID_ARG, "%s: negative size", fn);
   if (batch == 0 || rows == 0 || K == 0) return NVFP4MOE_OK;
-  NVFP4_REQUIRE(K <= INT32_MAX && rows <= INT32_MAX && batch <= INT32_MAX, NVFP4MOE_UNSUPPORTED_SHAPE,
-                "%s: a size above 2^31 - 1", fn);
+  NVFP4_REQUIRE(K <= INT32_MAX / 4 && rows <= INT32_MAX && batch <= INT32_MAX, NVFP4MOE_UNSUPPORTED_SHAPE,
+                "%s: K above 2^29 or another size above 2^31 - 1", fn);
   NVFP4_REQUIRE(x && codes && scale, NVFP4MOE_INVALID_ARG, "%s: NULL pointer", fn);
   const int64_t nb = fp8_blocks(K), srows = tile == NVFP4MOE_FP8_ROWS ? rows : fp8_blocks(rows);
   NVFP4_REQUIRE((rows == 1 || ldx >= K) && (rows == 1 || ldc >= K) && (srows == 1 || lds >= nb),
