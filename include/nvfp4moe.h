@@ -446,6 +446,12 @@ nvfp4moe_status fp8_gemm(const uint8_t* A, int64_t lda, const float* A_scale, in
  * ---------------------------------------------------------------------------- */
 typedef struct {
   int32_t T, H, I, E, top_k;
+  /* NVFP4MOE_LAUNCH_SINGLE: one persistent, cooperative launch (after a small one that zeroes its
+   * counters), for T <= 32 and rows of x that fit in shared memory beside three stages of weights
+   * (H <= 7168 at T <= 16, about half of that above), else NVFP4MOE_UNSUPPORTED_SHAPE;
+   * NVFP4MOE_LAUNCH_MULTI: routing, permutation, quantisation, grouped products and combine as
+   * launches of their own; NVFP4MOE_LAUNCH_AUTO: SINGLE where it fits. */
+  int32_t launch_mode;
   const uint8_t* w13_codes; /* [E][2][I][H]: gate, then up */
   const float* w13_scale;   /* [E][2][ceil(I/128)][ceil(H/128)] */
   const uint8_t* w2_codes;  /* [E][H][I] */

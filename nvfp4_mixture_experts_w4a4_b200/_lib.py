@@ -63,7 +63,7 @@ class MoeFfnWsLayout(ctypes.Structure):
 
 class Fp8MoeFfnDesc(ctypes.Structure):
     _fields_ = [
-        ("T", _i32), ("H", _i32), ("I", _i32), ("E", _i32), ("top_k", _i32),
+        ("T", _i32), ("H", _i32), ("I", _i32), ("E", _i32), ("top_k", _i32), ("launch_mode", _i32),
         ("w13_codes", _vp), ("w13_scale", _vp), ("w2_codes", _vp), ("w2_scale", _vp),
     ]
 

@@ -86,9 +86,10 @@ fp8_place_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict_
 
 struct Layout {
   int64_t ids, w, counts, offsets, padded, pair_to_row, row_token, row_pair, tile_expert, active, scratch, tiles,
-      x_codes, x_scale, h_codes, h_scale, slots, total;
+      x_codes, x_scale, h_codes, h_scale, slots, counters, parts, total;
   int64_t pairs;
   int max_row_tiles;
+  bool single;
 };
 
 nvfp4moe_status check_desc(const fp8_moe_ffn_desc* d, const char* fn) {
@@ -102,7 +103,17 @@ nvfp4moe_status check_desc(const fp8_moe_ffn_desc* d, const char* fn) {
   NVFP4_REQUIRE(d->top_k >= 1 && d->top_k <= 32 && d->top_k <= d->E, NVFP4MOE_UNSUPPORTED_SHAPE,
                 "%s: top_k=%d outside [1, min(E, 32)]", fn, d->top_k);
   NVFP4_REQUIRE(int64_t(d->T) * d->top_k <= (int64_t(1) << 24), NVFP4MOE_UNSUPPORTED_SHAPE, "%s: T*top_k > 2^24", fn);
+  NVFP4_REQUIRE(d->launch_mode == NVFP4MOE_LAUNCH_AUTO || d->launch_mode == NVFP4MOE_LAUNCH_SINGLE ||
+                    d->launch_mode == NVFP4MOE_LAUNCH_MULTI,
+                NVFP4MOE_INVALID_ARG, "%s: launch_mode=%d", fn, d->launch_mode);
+  NVFP4_REQUIRE(d->launch_mode != NVFP4MOE_LAUNCH_SINGLE || d->T == 0 || fp8_layer_fits(d->T, d->H, d->I, d->E, d->top_k),
+                NVFP4MOE_UNSUPPORTED_SHAPE, "%s: T=%d H=%d does not fit the single launch", fn, d->T, d->H);
   return NVFP4MOE_OK;
+}
+
+// One launch for the batches it fits, unless the caller says otherwise.
+bool takes_single(const fp8_moe_ffn_desc& d) {
+  return d.launch_mode != NVFP4MOE_LAUNCH_MULTI && d.T > 0 && fp8_layer_fits(d.T, d.H, d.I, d.E, d.top_k);
 }
 
 Layout make_layout(const fp8_moe_ffn_desc& d) {
@@ -116,6 +127,14 @@ Layout make_layout(const fp8_moe_ffn_desc& d) {
   const int64_t P = int64_t(d.T) * d.top_k, nH = fp8_blocks(d.H), nI = fp8_blocks(d.I);
   L.pairs = P;
   L.max_row_tiles = int(P / kRowTile + (P < d.E ? P : d.E));
+  L.single = takes_single(d);
+  if (L.single) {
+    const Fp8LayerSizes z = fp8_layer_sizes(d.T, d.H, d.I, d.E, d.top_k);
+    L.counters = put(z.counters * 4), L.parts = put(z.parts * 4), L.slots = put(z.slots * 4);
+    L.h_codes = put(z.h_codes), L.h_scale = put(z.h_scale * 4);
+    L.total = at;
+    return L;
+  }
   L.ids = put(P * 4), L.w = put(P * 4);
   L.counts = put(d.E * 4), L.offsets = put((d.E + 1) * 4), L.padded = put((d.E + 1) * 4);
   L.pair_to_row = put(P * 4), L.row_token = put(P * 4), L.row_pair = put(P * 4), L.tile_expert = put(P * 4);
@@ -160,6 +179,15 @@ nvfp4moe_status fp8_moe_ffn_forward(const fp8_moe_ffn_desc* desc, const void* x,
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   auto i32 = [&](int64_t at) { return reinterpret_cast<int32_t*>(ws + at); };
   auto f32 = [&](int64_t at) { return reinterpret_cast<float*>(ws + at); };
+  if (L.single) {
+    Fp8LayerCall c{};
+    c.x = x, c.logits = logits, c.out = out;
+    c.T = d.T, c.H = d.H, c.I = d.I, c.E = d.E, c.k = d.top_k;
+    c.w13_codes = d.w13_codes, c.w2_codes = d.w2_codes, c.w13_scale = d.w13_scale, c.w2_scale = d.w2_scale;
+    c.counters = i32(L.counters), c.parts = f32(L.parts), c.slots = f32(L.slots);
+    c.h_codes = ws + L.h_codes, c.h_scale = f32(L.h_scale);
+    return launch_fp8_layer(c, s);
+  }
   st = launch_batch_prologue(x, logits, d.T, d.H, d.E, d.top_k, 1, 0, nullptr, i32(L.ids), f32(L.w), i32(L.counts),
                              i32(L.offsets), i32(L.padded), i32(L.pair_to_row), i32(L.row_token), i32(L.row_pair),
                              i32(L.tile_expert), i32(L.active), nullptr, 1, nullptr, nullptr, ws + L.scratch, nullptr,

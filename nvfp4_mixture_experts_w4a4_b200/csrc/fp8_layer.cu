@@ -1,0 +1,763 @@
+// The whole FP8 routed layer in one persistent launch for batches of at most 32 tokens (after a
+// small launch that zeroes its counters): routing, x in E4M3, gate/up, SwiGLU, h in E4M3, down and
+// the combine in slot order.
+//
+// Such a batch is a stream of expert weights, 3 H I bytes per touched expert, against a few rows of
+// activations: its time is those bytes over the memory's rate plus what precedes and follows the
+// stream.  One CTA per SM routes the whole batch itself, so the stream starts as soon as the logits
+// have been read, and keeps x in shared memory as the MMA's B operand; the weights are its M side (128
+// rows), the batch its N side (16 or 32 columns).  A stage of the ring is two 128 x 128 tiles of
+// weights (32 KB) with a scale each:
+//   gate/up unit (expert, 128 columns of h): a gate and an up tile per block of H.  Its sums, with
+//     the scales of both operands applied in fp32 registers after every block, give 128 columns of h:
+//     one quantisation group a token, so nothing but done counters leaves the CTA.
+//   down unit (expert, 128 columns of the output): two tiles per stage, blocks 2j and 2j + 1 of I.
+//     Its h rows come back from L2 once the expert's gate/up units have counted up; the weights
+//     never wait, so the ring keeps streaming across the change.
+// Units go round-robin over the CTAs, gate/up first; CTAs with one gate/up unit less take the
+// first down units.  Where few experts are touched, gate/up units are split along H (the last
+// of a unit's parts to finish adds the parts in order) and down units along I (the combine adds them).
+// Combine: after a grid-wide barrier every CTA sums a slice of the outputs over the k slots of a
+// token, in slot order, and rounds once.
+//
+// Warps: 0 streams weights (TMA); 1 owns TMEM and issues the MMAs; 2 fetches scales, and h for down
+// stages; 4..7 add and finish the first tile of every stage, 8..11 the second; 3..15 quantise x first.
+// Every wait is bounded (status bit on timeout; copies in flight land before the CTA exits).
+#include "fp8.cuh"
+#include "fp8_tile.cuh"
+#include "tcgen05.cuh"
+#include "tma.cuh"
+#include "topk.cuh"
+
+namespace nvfp4moe {
+namespace {
+
+using namespace sm100;
+
+constexpr int kThreads = 512;
+constexpr int kTile = 128 * 128;         // bytes of a weight tile
+constexpr int kStage = 2 * kTile;
+constexpr int kMaxStages = 6, kMinStages = 3;
+constexpr int kSlots = 8;                // accumulator slots (stages in flight past the MMA)
+constexpr int kMaxE = 1024;
+constexpr int kPitch = 132;              // floats of a row of the exchange buffer
+constexpr int kSmemLimit = 226 * 1024;   // dynamic; a few hundred bytes more are static
+constexpr int kMaxSplit = 4;             // parts of a gate/up unit
+constexpr uint32_t kTimeout = NVFP4MOE_DEV_TIMEOUT;
+constexpr uint32_t kPolls = 1u << 22;
+
+__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+struct LayerArgs {
+  const __nv_bfloat16* x;
+  const float* logits;
+  int T, H, I, E, k;
+  int nH, nI;              // 128-blocks
+  int stages;
+  int max_parts;           // gate/up unit parts that `parts` holds
+  int chunks_cap;          // K chunks per pair that `slots` holds
+  const float* w13_scale;  // [E][2][nI][nH]
+  const float* w2_scale;   // [E][nH][nI]
+  uint8_t* h_codes;        // [pairs][I]
+  float* h_scale;          // [pairs][nI]
+  float* parts;            // [max_parts][2][NT][128]
+  float* slots;            // [pairs][s2][H]
+  int* done;               // [experts touched] finished gate/up units
+  int* tickets;            // [gate/up units] finished parts, where units are split
+  int* gbar;               // [1]
+  __nv_bfloat16* out;
+  uint32_t* status;
+};
+
+// Byte offsets in dynamic shared memory (1024-byte aligned base).
+struct Smem {
+  int h, x, xs, sb, hs, buf, mask, list, row0, rowof, ids, w, bars, total;
+};
+__host__ __device__ inline Smem smem_layout(int nt, int nH, int k, int E, int stages) {
+  Smem m;
+  int at = stages * kStage;
+  auto put = [&](int bytes) {
+    const int here = at;
+    at += (bytes + 15) / 16 * 16;
+    return here;
+  };
+  m.h = put(stages * 2 * nt * 128);
+  m.x = put(nH * nt * 128);
+  m.xs = put(nH * nt * 4);
+  m.sb = put(kSlots * 2 * 4);
+  m.hs = put(kSlots * 2 * nt * 4);
+  m.buf = put(nt * kPitch * 4);
+  const int most = nt * k < E ? nt * k : E;
+  m.mask = put(E * 4);
+  m.rowof = put(E * 4);
+  m.list = put(most * 4);
+  m.row0 = put((most + 1) * 4);
+  m.ids = put(nt * k * 4);
+  m.w = put(nt * k * 4);
+  m.bars = put((2 * kMaxStages + 2 * kSlots + 4) * 8);
+  m.total = at + 1024;
+  return m;
+}
+
+// The schedule, the same in every thread of every CTA: it follows from the number of experts
+// touched (A) and the grid.
+struct Plan {
+  int A, G, s1, s2, n1, n2, extra, light, heavy, first2;
+  __device__ Plan(const LayerArgs& a, int active, int grid, int cta) {
+    A = active, G = grid;
+    s1 = 1, s2 = 1;
+    const int u1 = A * a.nI, u2 = A * a.nH, st2 = ceil_div(a.nI, 2);
+    // Parts of a unit: the count with the fewest stages in the fullest CTA, a part costing two
+    // stages more than its own.
+    if (u1 < G) {
+      int least = INT32_MAX;
+      for (int s = 1; s <= kMaxSplit && s <= a.nH && u1 * s <= a.max_parts; ++s) {
+        const int cost = ceil_div(u1 * s, G) * (ceil_div(a.nH, s) + (s > 1 ? 2 : 0));
+        if (cost < least) least = cost, s1 = s;
+      }
+    }
+    if (u2 < 4 * G) {
+      int least = INT32_MAX;
+      for (int s = 1; s <= a.chunks_cap && s <= st2; ++s) {
+        const int cost = ceil_div(u2 * s, G) * (ceil_div(st2, s) + 1);
+        if (cost < least) least = cost, s2 = s;
+      }
+    }
+    const int U1 = u1 * s1, U2 = u2 * s2;
+    heavy = U1 % G;
+    light = G - heavy;
+    n1 = U1 / G + (cta < heavy ? 1 : 0);
+    extra = heavy > 0 ? min(ceil_div(a.nH, s1) / ceil_div(st2, s2), U2 / light) : 0;
+    const int rest = U2 - extra * light;
+    first2 = (cta + G - heavy) % G;  // place among the CTAs that share the rest: light ones first
+    n2 = (cta >= heavy ? extra : 0) + rest / G + (first2 < rest % G ? 1 : 0);
+  }
+  __device__ int units() const { return n1 + n2; }
+};
+
+struct Unit {
+  bool down;
+  int a;         // index of the expert among the touched
+  int blk;       // 128-block of I (gate/up) or of H (down)
+  int part;      // K part
+  int id;        // gate/up: unit index without the part
+  int j0, j1;    // stages: blocks of H, or pairs of blocks of I
+};
+
+__device__ __forceinline__ Unit unit_of(const Plan& p, const LayerArgs& a, int i, int cta) {
+  Unit u;
+  u.down = i >= p.n1;
+  if (!u.down) {
+    const int id = cta + i * p.G;
+    u.id = id / p.s1;
+    u.part = id - u.id * p.s1;
+    u.a = u.id / a.nI;
+    u.blk = u.id - u.a * a.nI;
+    u.j0 = a.nH * u.part / p.s1;
+    u.j1 = a.nH * (u.part + 1) / p.s1;
+  } else {
+    int r = i - p.n1, id;
+    if (cta >= p.heavy && r < p.extra) {
+      id = r * p.light + cta - p.heavy;
+    } else {
+      if (cta >= p.heavy) r -= p.extra;
+      id = p.extra * p.light + r * p.G + p.first2;
+    }
+    const int v = id / p.s2, st2 = ceil_div(a.nI, 2);
+    u.part = id - v * p.s2;
+    u.a = v / a.nH;
+    u.blk = v - u.a * a.nH;
+    u.id = v;
+    u.j0 = st2 * u.part / p.s2;
+    u.j1 = st2 * (u.part + 1) / p.s2;
+  }
+  return u;
+}
+
+__device__ __forceinline__ void load_tile(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}"
+      ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(0u)
+      : "memory");
+}
+__device__ __forceinline__ int load_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void add_release(int* p) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p) : "memory");
+}
+// Waits until *p >= want; false when it gave up.
+__device__ __forceinline__ bool wait_count(const int* p, int want) {
+  for (uint32_t i = 0; i < kPolls; ++i) {
+    if (load_acquire(p) >= want) return true;
+    __nanosleep(32);
+  }
+  return false;
+}
+__device__ __forceinline__ void add_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <int NT>
+__device__ __forceinline__ void read_columns(uint32_t taddr, uint32_t (&r)[NT]) {
+  if constexpr (NT == 32) {
+    tmem_ld_32x32b_x32(taddr, r);
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+  }
+  tmem_ld_wait();
+}
+
+__global__ void fp8_layer_reset_kernel(int* counters, int n) {
+  griddep_launch_dependents();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) counters[i] = 0;
+}
+
+template <int NT, int PER_LANE>
+__global__ void __launch_bounds__(kThreads, 1)
+fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant__ CUtensorMap tm2,
+                 const __grid_constant__ CUtensorMap tmh, const LayerArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_shared_1024(smem_raw);
+  const Smem m = smem_layout(NT, a.nH, a.k, a.E, a.stages);
+  float* s_xs = reinterpret_cast<float*>(smem + m.xs);          // [nH][NT]
+  float* s_sb = reinterpret_cast<float*>(smem + m.sb);          // [slot][2]
+  float* s_hs = reinterpret_cast<float*>(smem + m.hs);          // [slot][2][NT]
+  float* s_buf = reinterpret_cast<float*>(smem + m.buf);        // [NT][kPitch]
+  uint32_t* s_mask = reinterpret_cast<uint32_t*>(smem + m.mask);  // [E] tokens of each expert
+  int* s_rowof = reinterpret_cast<int*>(smem + m.rowof);        // [E] first pair row of the expert
+  int* s_list = reinterpret_cast<int*>(smem + m.list);          // touched experts, ascending
+  int* s_row0 = reinterpret_cast<int*>(smem + m.row0);          // their first pair rows, then the end
+  int* s_ids = reinterpret_cast<int*>(smem + m.ids);            // [T][k]
+  float* s_w = reinterpret_cast<float*>(smem + m.w);            // [T][k]
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + m.bars);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* acc_full = empty + kMaxStages;
+  uint64_t* acc_empty = acc_full + kSlots;
+  uint64_t* x_full = acc_empty + kSlots;
+  uint64_t* drain = x_full + 1;
+  __shared__ uint32_t tmem_holder;
+  __shared__ volatile int abort_flag;
+  __shared__ int s_active, s_scan[2][kThreads / 32], s_last;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
+  constexpr int XWARPS = kThreads / 32 - 3;
+
+  // ---- set-up, with the logits on their way ----
+  constexpr int TOK = NT / 16;  // tokens a warp routes
+  float lg[TOK][PER_LANE];
+#pragma unroll
+  for (int i = 0; i < TOK; ++i) {
+    const int t = warp + 16 * i;
+#pragma unroll
+    for (int j = 0; j < PER_LANE; ++j) {
+      const int e = lane + 32 * j;
+      lg[i][j] = t < a.T && e < a.E ? __ldg(a.logits + int64_t(t) * a.E + e) : 0.0f;
+    }
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(&full[s], 2);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&acc_full[s], 1);
+      mbar_init(&acc_empty[s], 8);
+    }
+    mbar_init(x_full, XWARPS * 32);
+    mbar_init(drain, 1);
+    abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_holder, kSlots * 2 * NT);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 64) {
+    prefetch_tensormap(&tm13);
+    prefetch_tensormap(&tm2);
+    prefetch_tensormap(&tmh);
+  }
+  for (int e = threadIdx.x; e < a.E; e += kThreads) s_mask[e] = 0u;
+  __syncthreads();
+
+  // ---- routing and the list of touched experts ----
+#pragma unroll
+  for (int i = 0; i < TOK; ++i) {
+    const int t = warp + 16 * i;
+    if (t < a.T) {
+      int id;
+      float wt;
+      warp_topk_regs<PER_LANE>(lg[i], a.E, a.k, &id, &wt);
+      if (lane < a.k) {
+        s_ids[t * a.k + lane] = id;
+        s_w[t * a.k + lane] = wt;
+        atomicOr(&s_mask[id], 1u << t);
+      }
+    }
+  }
+  __syncthreads();
+  {
+    static_assert(kMaxE == 2 * kThreads, "two experts a thread");
+    int n[2], act = 0, rows = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = 2 * int(threadIdx.x) + i;
+      n[i] = e < a.E ? __popc(s_mask[e]) : 0;
+      act += n[i] > 0;
+      rows += n[i];
+    }
+    int ia = act, ir = rows;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, ia, o), z = __shfl_up_sync(0xffffffffu, ir, o);
+      if (lane >= o) ia += y, ir += z;
+    }
+    if (lane == 31) s_scan[0][warp] = ia, s_scan[1][warp] = ir;
+    __syncthreads();
+    ia -= act, ir -= rows;
+    for (int w = 0; w < warp; ++w) ia += s_scan[0][w], ir += s_scan[1][w];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = 2 * int(threadIdx.x) + i;
+      if (n[i] > 0) {
+        s_list[ia] = e;
+        s_row0[ia] = ir;
+        s_rowof[e] = ir;
+        ++ia, ir += n[i];
+      }
+    }
+    if (threadIdx.x == kThreads - 1) {
+      s_active = ia;
+      s_row0[ia] = ir;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_holder;
+  const Plan p(a, s_active, int(gridDim.x), cta);
+  const int units = p.units();
+  const int S = a.stages;
+  auto abort_now = [&]() {
+    abort_flag = 1;
+    atomicOr(a.status, kTimeout);
+  };
+
+  // ---- x in E4M3, in the MMA's layout: eight lanes a group of 128 ----
+  if (warp >= 3) {
+    const int sub = lane & 7;
+    const int groups = a.T * a.nH;
+    for (int g0 = (warp - 3) * 4; g0 < groups; g0 += XWARPS * 4) {
+      const int g = g0 + (lane >> 3);
+      const int t = g / a.nH, kb = g - t * a.nH;
+      uint32_t u[2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int c = kb * 128 + (sub + 8 * j) * 8;
+        uint4 q = make_uint4(0u, 0u, 0u, 0u);
+        if (g < groups && c < a.H) q = __ldg(reinterpret_cast<const uint4*>(a.x + int64_t(t) * a.H + c));
+        u[j][0] = q.x, u[j][1] = q.y, u[j][2] = q.z, u[j][3] = q.w;
+      }
+      uint32_t mx = 0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx = __vmaxu2(mx, u[j][i] & 0x7FFF7FFFu);
+      mx = max(mx << 16, mx & 0xFFFF0000u);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const Fp8ScaleBf16 f = fp8_scale_bf16(mx);
+      if (g < groups) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t w[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float v[4];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              v[2 * q] = __uint_as_float(u[j][2 * i + q] << 16);
+              v[2 * q + 1] = __uint_as_float(u[j][2 * i + q] & 0xFFFF0000u);
+            }
+            w[i] = fp8_encode4(v, f);
+          }
+          // 128-byte rows, 16-byte pieces exchanged by the row's low three bits
+          const int piece = (sub + 8 * j) >> 1;
+          uint8_t* dst = smem + m.x + kb * NT * 128 + t * 128 + ((piece ^ (t & 7)) << 4) + (sub & 1) * 8;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+        }
+        if (sub == 0) s_xs[kb * NT + t] = f.scale;
+      }
+    }
+    fence_proxy_async_shared();
+    mbar_arrive(x_full);
+  }
+
+  if (warp == 0) {
+    if (elect_one()) {
+      uint32_t it = 0;
+      for (int i = 0; i < units && !abort_flag; ++i) {
+        const Unit u = unit_of(p, a, i, cta);
+        const int e = s_list[u.a];
+        for (int j = u.j0; j < u.j1; ++j, ++it) {
+          const int s = it % S;
+          if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1)) {
+            abort_now();
+            break;
+          }
+          uint8_t* dst = smem + s * kStage;
+          mbar_arrive_expect_tx(&full[s], kStage);
+          if (u.down) {
+            load_tile(dst, &tm2, 2 * j * 128, u.blk * 128, e, &full[s]);
+            load_tile(dst + kTile, &tm2, (2 * j + 1) * 128, u.blk * 128, e, &full[s]);
+          } else {
+            load_tile(dst, &tm13, j * 128, u.blk * 128, 2 * e, &full[s]);
+            load_tile(dst + kTile, &tm13, j * 128, u.blk * 128, 2 * e + 1, &full[s]);
+          }
+        }
+      }
+      if (abort_flag)
+        for (uint32_t back = 0; back < uint32_t(S) && back < it; ++back) {
+          const uint32_t j = it - 1 - back;
+          mbar_wait(&full[j % S], (j / S) & 1, 1u << 16);
+        }
+    }
+  } else if (warp == 1) {
+    if (elect_one()) {
+      constexpr uint32_t idesc = (1u << 4) | (uint32_t(NT >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+      uint32_t it = 0;
+      bool ok = mbar_wait(x_full, 0);
+      if (!ok) abort_now();
+      for (int i = 0; i < units && ok && !abort_flag; ++i) {
+        const Unit u = unit_of(p, a, i, cta);
+        for (int j = u.j0; j < u.j1; ++j, ++it) {
+          const int s = it % S, slot = it % kSlots;
+          if (!mbar_wait(&acc_empty[slot], ((it / kSlots) & 1) ^ 1) || !mbar_wait(&full[s], (it / S) & 1)) {
+            abort_now();
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint64_t ad = desc_kmajor_sw128(smem + s * kStage + h * kTile);
+            const uint64_t bd = desc_kmajor_sw128(u.down ? smem + m.h + (2 * s + h) * NT * 128 : smem + m.x + j * NT * 128);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              mma_f8(tmem + (2 * slot + h) * NT, ad + 2 * q, bd + 2 * q, idesc, q != 0 ? 1u : 0u);
+          }
+          tc_commit(&empty[s]);
+          tc_commit(&acc_full[slot]);
+        }
+      }
+      tc_commit(drain);
+      mbar_wait(drain, 0, 1u << 20);
+    }
+  } else if (warp == 2) {
+    // scales of the stage's two tiles, and for down stages h and its scales
+    uint32_t it = 0;
+    bool waited = false;  // for the launch that zeroed the counters
+    int have = -1;        // the expert whose h is known to be complete
+    for (int i = 0; i < units && !abort_flag; ++i) {
+      const Unit u = unit_of(p, a, i, cta);
+      const int e = s_list[u.a], row0 = s_row0[u.a], n = s_row0[u.a + 1] - row0;
+      if (u.down && u.a != have) {
+        if (!waited) griddep_wait(), waited = true;
+        if (!wait_count(a.done + u.a, a.nI)) {
+          abort_now();
+          break;
+        }
+        have = u.a;
+        asm volatile("fence.proxy.async;" ::: "memory");  // h was written by ordinary stores
+      }
+      bool ok = true;
+      for (int j = u.j0; j < u.j1; ++j, ++it) {
+        const int s = it % S, slot = it % kSlots;
+        float sb = 0.0f, hs[2] = {0.0f, 0.0f};
+        if (u.down) {
+          if (lane < 2 && 2 * j + lane < a.nI) sb = __ldg(a.w2_scale + (int64_t(e) * a.nH + u.blk) * a.nI + 2 * j + lane);
+          if (lane < n) {
+            const float* q = a.h_scale + int64_t(row0 + lane) * a.nI + 2 * j;
+            hs[0] = __ldcg(q);
+            if (2 * j + 1 < a.nI) hs[1] = __ldcg(q + 1);
+          }
+        } else if (lane < 2) {
+          sb = __ldg(a.w13_scale + ((int64_t(e) * 2 + lane) * a.nI + u.blk) * a.nH + j);
+        }
+        if (!mbar_wait(&acc_empty[slot], ((it / kSlots) & 1) ^ 1) || !mbar_wait(&empty[s], ((it / S) & 1) ^ 1)) {
+          abort_now();
+          ok = false;
+          break;
+        }
+        if (lane < 2) s_sb[2 * slot + lane] = sb;
+        if (u.down && lane < NT) {
+          s_hs[(2 * slot) * NT + lane] = hs[0];
+          s_hs[(2 * slot + 1) * NT + lane] = hs[1];
+        }
+        __syncwarp();
+        if (lane == 0) {
+          if (u.down) {
+            mbar_arrive_expect_tx(&full[s], 2 * NT * 128);
+            load_tile(smem + m.h + 2 * s * NT * 128, &tmh, 2 * j * 128, row0, 0, &full[s]);
+            load_tile(smem + m.h + (2 * s + 1) * NT * 128, &tmh, (2 * j + 1) * 128, row0, 0, &full[s]);
+          } else {
+            mbar_arrive(&full[s]);
+          }
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+    }
+    if (!waited) griddep_wait();
+  } else if (warp >= 4 && warp < 12) {
+    const int half = (warp - 4) >> 2, q = warp & 3, r = q * 32 + lane;
+    const uint32_t trow = tmem + (uint32_t(q * 32) << 16);
+    bool ok = mbar_wait(x_full, 0);
+    if (!ok) abort_now();
+    griddep_wait();  // the counters are zero
+    uint32_t it = 0;
+    for (int i = 0; i < units && ok; ++i) {
+      const Unit u = unit_of(p, a, i, cta);
+      const int e = s_list[u.a], row0 = s_row0[u.a], n = s_row0[u.a + 1] - row0;
+      float acc[NT];
+#pragma unroll
+      for (int c = 0; c < NT; ++c) acc[c] = 0.0f;
+      for (int j = u.j0; j < u.j1; ++j, ++it) {
+        const int slot = it % kSlots;
+        if (abort_flag || !mbar_wait(&acc_full[slot], (it / kSlots) & 1)) {
+          abort_now();
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t v[NT];
+        read_columns<NT>(trow + (2 * slot + half) * NT, v);
+        const float sb = s_sb[2 * slot + half];
+        const float4* sc = reinterpret_cast<const float4*>(u.down ? s_hs + (2 * slot + half) * NT : s_xs + j * NT);
+#pragma unroll
+        for (int c = 0; c < NT; c += 4) {
+          const float4 f = sc[c / 4];
+          acc[c] = fmaf(__uint_as_float(v[c]), f.x * sb, acc[c]);
+          acc[c + 1] = fmaf(__uint_as_float(v[c + 1]), f.y * sb, acc[c + 1]);
+          acc[c + 2] = fmaf(__uint_as_float(v[c + 2]), f.z * sb, acc[c + 2]);
+          acc[c + 3] = fmaf(__uint_as_float(v[c + 3]), f.w * sb, acc[c + 3]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acc_empty[slot]);
+      }
+      if (!ok) break;
+      if (u.down) {
+        // both halves' sums are one output: the second hands its over
+        if (half == 1) {
+#pragma unroll
+          for (int c = 0; c < NT; ++c)
+            if (c < n) s_buf[c * kPitch + r] = acc[c];
+        }
+        add_barrier();
+        const int col = u.blk * 128 + r;
+        if (half == 0 && col < a.H) {
+          float* dst = a.slots + (int64_t(row0) * p.s2 + u.part) * a.H + col;
+#pragma unroll
+          for (int c = 0; c < NT; ++c)
+            if (c < n) dst[int64_t(c) * p.s2 * a.H] = acc[c] + s_buf[c * kPitch + r];
+        }
+        add_barrier();
+      } else {
+        bool finish = true;
+        if (p.s1 > 1) {
+          // this part's sums; the last part to arrive adds all of them in order
+          float* dst = a.parts + ((int64_t(u.id) * p.s1 + u.part) * 2 + half) * NT * 128 + r;
+#pragma unroll
+          for (int c = 0; c < NT; ++c)
+            if (c < a.T) __stcg(dst + c * 128, acc[c]);
+          __threadfence();
+          add_barrier();
+          if (threadIdx.x == 128) {
+            const int before = atomicAdd(a.tickets + u.id, 1);
+            __threadfence();
+            s_last = before == p.s1 - 1;
+          }
+          add_barrier();
+          finish = s_last != 0;
+          if (finish) {
+#pragma unroll
+            for (int c = 0; c < NT; ++c) acc[c] = 0.0f;
+            for (int k = 0; k < p.s1; ++k) {
+              const float* src = a.parts + ((int64_t(u.id) * p.s1 + k) * 2 + half) * NT * 128 + r;
+#pragma unroll
+              for (int c = 0; c < NT; ++c)
+                if (c < a.T) acc[c] += __ldcg(src + c * 128);
+            }
+          }
+        }
+        if (finish) {
+          if (half == 1) {
+#pragma unroll
+            for (int c = 0; c < NT; ++c) s_buf[c * kPitch + r] = acc[c];
+          }
+          add_barrier();
+          if (half == 0) {
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+              s_buf[c * kPitch + r] = __fdividef(acc[c], 1.0f + __expf(-acc[c])) * s_buf[c * kPitch + r];
+          }
+          add_barrier();
+          // a warp takes every eighth token of the expert: 128 columns, one group
+          const uint32_t mask = s_mask[e];
+          const int i0 = u.blk * 128 + lane * 4;
+          for (int c = warp - 4; c < n; c += 8) {
+            const int t = __fns(mask, 0, c + 1);  // the token's column
+            const float4 h = *reinterpret_cast<const float4*>(s_buf + t * kPitch + lane * 4);
+            const uint32_t mx = __reduce_max_sync(
+                0xffffffffu, max(max(abs_bits(h.x), abs_bits(h.y)), max(abs_bits(h.z), abs_bits(h.w))));
+            const Fp8Scale f = fp8_scale(mx);
+            const float v[4] = {h.x, h.y, h.z, h.w};
+            const uint32_t codes = fp8_encode4(v, f);
+            if (i0 < a.I) *reinterpret_cast<uint32_t*>(a.h_codes + int64_t(row0 + c) * a.I + i0) = codes;
+            if (lane == 0) a.h_scale[int64_t(row0 + c) * a.nI + u.blk] = f.scale;
+          }
+          __threadfence();
+          add_barrier();
+          if (threadIdx.x == 128) add_release(a.done + u.a);
+        }
+      }
+    }
+    // ---- combine ----
+    __threadfence();
+    add_barrier();
+    if (threadIdx.x == 128) {
+      add_release(a.gbar);
+      if (!wait_count(a.gbar, int(gridDim.x))) abort_now();
+    }
+    add_barrier();
+    if (!abort_flag) {
+      const int per_row = a.H / 4;
+      const int total = a.T * per_row, stride = int(gridDim.x) * 256;
+      for (int i = cta * 256 + int(threadIdx.x) - 128; i < total; i += stride) {
+        const int t = i / per_row, c = (i - t * per_row) * 4;
+        const uint32_t below = (1u << t) - 1u;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int j = 0; j < a.k; ++j) {
+          const int id = s_ids[t * a.k + j];
+          const float w = s_w[t * a.k + j];
+          const float* src = a.slots + int64_t(s_rowof[id] + __popc(s_mask[id] & below)) * p.s2 * a.H + c;
+          float4 z = __ldcg(reinterpret_cast<const float4*>(src));
+          for (int k = 1; k < p.s2; ++k) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + int64_t(k) * a.H));
+            z.x += v.x, z.y += v.y, z.z += v.z, z.w += v.w;
+          }
+          y.x = fmaf(w, z.x, y.x), y.y = fmaf(w, z.y, y.y), y.z = fmaf(w, z.z, y.z), y.w = fmaf(w, z.w, y.w);
+        }
+        const __nv_bfloat162 o0 = __floats2bfloat162_rn(y.x, y.y), o1 = __floats2bfloat162_rn(y.z, y.w);
+        *reinterpret_cast<uint2*>(a.out + int64_t(t) * a.H + c) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&o0), *reinterpret_cast<const uint32_t*>(&o1));
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kSlots * 2 * NT);
+}
+
+int columns_for(int T) { return T <= 16 ? 16 : 32; }
+int stages_for(int T, int H, int E, int k) {
+  for (int s = kMaxStages; s >= kMinStages; --s)
+    if (smem_layout(columns_for(T), int(fp8_blocks(H)), k, E, s).total <= kSmemLimit) return s;
+  return 0;
+}
+// K chunks of a down unit at most: enough for the fewest units there can be (one expert)
+int chunks_for(int H, int I) {
+  const int st2 = int((fp8_blocks(I) + 1) / 2);
+  int c = (4 * 148 + int(fp8_blocks(H)) - 1) / int(fp8_blocks(H));
+  return c < 1 ? 1 : (c > st2 ? st2 : (c > 8 ? 8 : c));
+}
+constexpr int kMaxParts = 4 * 148;
+
+template <int NT, int PER_LANE>
+cudaError_t launch_one(const CUtensorMap& m13, const CUtensorMap& m2, const CUtensorMap& mh, const LayerArgs& a,
+                       int grid, size_t smem, cudaStream_t s) {
+  constexpr auto kern = fp8_layer_kernel<NT, PER_LANE>;
+  const cudaError_t e = set_smem_limit_once<kern>(kSmemLimit);
+  return e != cudaSuccess ? e : launch_cooperative_dependent(kern, dim3(grid), dim3(kThreads), smem, s, m13, m2, mh, a);
+}
+
+template <int NT>
+cudaError_t launch_columns(const CUtensorMap& m13, const CUtensorMap& m2, const CUtensorMap& mh, const LayerArgs& a,
+                           int grid, size_t smem, cudaStream_t s) {
+  const int per = (a.E + 31) / 32;
+  if (per <= 1) return launch_one<NT, 1>(m13, m2, mh, a, grid, smem, s);
+  if (per <= 4) return launch_one<NT, 4>(m13, m2, mh, a, grid, smem, s);
+  if (per <= 8) return launch_one<NT, 8>(m13, m2, mh, a, grid, smem, s);
+  if (per <= 16) return launch_one<NT, 16>(m13, m2, mh, a, grid, smem, s);
+  return launch_one<NT, 32>(m13, m2, mh, a, grid, smem, s);
+}
+
+}  // namespace
+
+bool fp8_layer_fits(int T, int H, int I, int E, int k) {
+  return T >= 1 && T <= 32 && stages_for(T, H, E, k) > 0 && int64_t(E) * ((fp8_blocks(I) > fp8_blocks(H) ? fp8_blocks(I) : fp8_blocks(H))) < (1 << 27);
+}
+
+Fp8LayerSizes fp8_layer_sizes(int T, int H, int I, int E, int k) {
+  const int64_t P = int64_t(T) * k, nI = fp8_blocks(I);
+  const int64_t touched = P < E ? P : E;
+  Fp8LayerSizes z;
+  z.counters = touched + kMaxParts + 1;
+  z.parts = int64_t(kMaxParts) * 2 * columns_for(T) * 128;
+  z.slots = P * chunks_for(H, I) * H;
+  z.h_codes = P * I;
+  z.h_scale = P * nI;
+  return z;
+}
+
+nvfp4moe_status launch_fp8_layer(const Fp8LayerCall& c, cudaStream_t s) {
+  LayerArgs a{};
+  a.x = static_cast<const __nv_bfloat16*>(c.x);
+  a.logits = c.logits;
+  a.T = c.T, a.H = c.H, a.I = c.I, a.E = c.E, a.k = c.k;
+  a.nH = int(fp8_blocks(c.H)), a.nI = int(fp8_blocks(c.I));
+  a.stages = stages_for(c.T, c.H, c.E, c.k);
+  a.max_parts = kMaxParts;
+  a.chunks_cap = chunks_for(c.H, c.I);
+  a.w13_scale = c.w13_scale, a.w2_scale = c.w2_scale;
+  a.h_codes = c.h_codes, a.h_scale = c.h_scale, a.parts = c.parts, a.slots = c.slots;
+  const int touched = c.T * c.k < c.E ? c.T * c.k : c.E;
+  a.done = c.counters, a.tickets = c.counters + touched, a.gbar = c.counters + touched + kMaxParts;
+  a.out = static_cast<__nv_bfloat16*>(c.out);
+  a.status = device_status_ptr();
+  if (!a.status) return fail(NVFP4MOE_CUDA_ERROR, "device status word unavailable");
+  const int nt = columns_for(c.T);
+  CUtensorMap m13, m2, mh;
+  nvfp4moe_status st = make_fp8_map(&m13, c.w13_codes, c.H, c.I, 2 * int64_t(c.E), c.H, int64_t(c.I) * c.H, 128);
+  if (st == NVFP4MOE_OK) st = make_fp8_map(&m2, c.w2_codes, c.I, c.H, c.E, c.I, int64_t(c.I) * c.H, 128);
+  if (st == NVFP4MOE_OK) st = make_fp8_map(&mh, c.h_codes, c.I, int64_t(c.T) * c.k, 1, c.I, c.I, nt);
+  if (st != NVFP4MOE_OK) return st;
+  fp8_layer_reset_kernel<<<1, 512, 0, s>>>(c.counters, touched + kMaxParts + 1);
+  const size_t smem = smem_layout(nt, a.nH, c.k, c.E, a.stages).total;
+  const cudaError_t e = nt == 16 ? launch_columns<16>(m13, m2, mh, a, num_sms(), smem, s)
+                                 : launch_columns<32>(m13, m2, mh, a, num_sms(), smem, s);
+  if (e != cudaSuccess) return fail(NVFP4MOE_CUDA_ERROR, "fp8 layer: %s", cudaGetErrorString(e));
+  return check_launch("fp8 layer");
+}
+
+}  // namespace nvfp4moe

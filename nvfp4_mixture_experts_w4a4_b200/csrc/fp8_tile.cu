@@ -624,23 +624,6 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   }
 }
 
-// [mats][rows][K] bytes, rows `pitch` apart and matrices `mat_pitch`; box 128 bytes x box_rows,
-// 128-byte swizzle.  Rows and bytes past the ends read as zero.
-nvfp4moe_status make_map(CUtensorMap* map, const void* base, int64_t K, int64_t rows, int64_t mats, int64_t pitch,
-                         int64_t mat_pitch, int box_rows) {
-  auto fn = tensor_map_encoder();
-  if (!fn) return fail(NVFP4MOE_CUDA_ERROR, "cuTensorMapEncodeTiled is unavailable");
-  const cuuint64_t dims[3] = {cuuint64_t(K), cuuint64_t(rows), cuuint64_t(mats)};
-  const cuuint64_t strides[2] = {cuuint64_t(pitch), cuuint64_t(mat_pitch)};
-  const cuuint32_t box[3] = {cuuint32_t(TK), cuuint32_t(box_rows), 1u};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
-                        estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(NVFP4MOE_CUDA_ERROR, "cuTensorMapEncodeTiled failed (%d)", int(r));
-  return NVFP4MOE_OK;
-}
-
 template <int MODE, int BN, bool SPLIT, bool PAIR>
 cudaError_t launch_tiles(const CUtensorMap& a, const CUtensorMap& b, const TileParams& p, int grid, cudaStream_t s) {
   constexpr auto kern = fp8_tile_kernel<MODE, BN, SPLIT, PAIR>;
@@ -671,6 +654,23 @@ cudaError_t launch_tiles(const CUtensorMap& a, const CUtensorMap& b, const TileP
 }
 
 }  // namespace
+
+// [mats][rows][K] bytes, rows `pitch` apart and matrices `mat_pitch`; box 128 bytes x box_rows,
+// 128-byte swizzle.  Rows and bytes past the ends read as zero.
+nvfp4moe_status make_fp8_map(CUtensorMap* map, const void* base, int64_t K, int64_t rows, int64_t mats, int64_t pitch,
+                         int64_t mat_pitch, int box_rows) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return fail(NVFP4MOE_CUDA_ERROR, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint64_t dims[3] = {cuuint64_t(K), cuuint64_t(rows), cuuint64_t(mats)};
+  const cuuint64_t strides[2] = {cuuint64_t(pitch), cuuint64_t(mat_pitch)};
+  const cuuint32_t box[3] = {cuuint32_t(FP8_BLOCK), cuuint32_t(box_rows), 1u};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+                        estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(NVFP4MOE_CUDA_ERROR, "cuTensorMapEncodeTiled failed (%d)", int(r));
+  return NVFP4MOE_OK;
+}
 
 // How a dense product is run: the column width of a tile and the K split.  The estimate is rounds
 // of resident CTAs times the blocks a CTA runs, at the cost of one block: a tile of 256 columns
@@ -715,8 +715,8 @@ nvfp4moe_status launch_fp8_dense(const uint8_t* A, int64_t lda, const float* A_s
   p.status = device_status_ptr();
   if (!p.status) return fail(NVFP4MOE_CUDA_ERROR, "device status word unavailable");
   CUtensorMap am, bm;
-  nvfp4moe_status st = make_map(&am, A, K, M, 1, lda, lda, p.a_box);
-  if (st == NVFP4MOE_OK) st = make_map(&bm, B, K, N, 1, ldb, ldb, b_rows(plan.bn, plan.pair));
+  nvfp4moe_status st = make_fp8_map(&am, A, K, M, 1, lda, lda, p.a_box);
+  if (st == NVFP4MOE_OK) st = make_fp8_map(&bm, B, K, N, 1, ldb, ldb, b_rows(plan.bn, plan.pair));
   if (st != NVFP4MOE_OK) return st;
   const int64_t tiles = int64_t(p.n_mt) * p.n_nt;
   const int ctas = plan.pair ? 2 : plan.split;  // of one tile
@@ -740,11 +740,11 @@ nvfp4moe_status launch_fp8_grouped(const GroupedArgs& g, cudaStream_t s) {
   if (!status) return fail(NVFP4MOE_CUDA_ERROR, "device status word unavailable");
   const int nI = int(fp8_blocks(g.I)), nH = int(fp8_blocks(g.H));
   CUtensorMap xm, w13, hm, w2;
-  nvfp4moe_status st = make_map(&xm, g.x_codes, g.H, g.rows, 1, g.H, g.H, 32);
+  nvfp4moe_status st = make_fp8_map(&xm, g.x_codes, g.H, g.rows, 1, g.H, g.H, 32);
   if (st == NVFP4MOE_OK)
-    st = make_map(&w13, g.w13_codes, g.H, g.I, 2 * int64_t(g.E), g.H, int64_t(g.I) * g.H, TM);
-  if (st == NVFP4MOE_OK) st = make_map(&hm, g.h_codes, g.I, g.rows, 1, g.I, g.I, 32);
-  if (st == NVFP4MOE_OK) st = make_map(&w2, g.w2_codes, g.I, g.H, g.E, g.I, int64_t(g.I) * g.H, 256);
+    st = make_fp8_map(&w13, g.w13_codes, g.H, g.I, 2 * int64_t(g.E), g.H, int64_t(g.I) * g.H, TM);
+  if (st == NVFP4MOE_OK) st = make_fp8_map(&hm, g.h_codes, g.I, g.rows, 1, g.I, g.I, 32);
+  if (st == NVFP4MOE_OK) st = make_fp8_map(&w2, g.w2_codes, g.I, g.H, g.E, g.I, int64_t(g.I) * g.H, 256);
   if (st != NVFP4MOE_OK) return st;
   TileParams p{};
   p.a_box = 32;

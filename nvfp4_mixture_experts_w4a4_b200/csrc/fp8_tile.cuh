@@ -1,6 +1,8 @@
 // Launch interface of the FP8 tile kernel (fp8_tile.cu).
 #pragma once
 
+#include <cuda.h>
+
 #include "common.cuh"
 
 namespace nvfp4moe {
@@ -54,5 +56,31 @@ struct GroupedArgs {
   float* slots;              // [rows][H]
 };
 nvfp4moe_status launch_fp8_grouped(const GroupedArgs& g, cudaStream_t s);
+
+// Tensor map of E4M3 matrices [mats][rows][K], rows `pitch` bytes apart and matrices `mat_pitch`; box
+// 128 bytes x box_rows, 128-byte swizzle.  Rows and bytes past the ends read as zero.
+nvfp4moe_status make_fp8_map(CUtensorMap* map, const void* base, int64_t K, int64_t rows, int64_t mats, int64_t pitch,
+                             int64_t mat_pitch, int box_rows);
+
+// The whole layer in one persistent launch, for batches of at most 32 tokens (fp8_layer.cu).
+struct Fp8LayerSizes {
+  int64_t counters, parts, slots, h_codes, h_scale;  // elements (int, float, float, byte, float)
+};
+struct Fp8LayerCall {
+  const void* x;
+  const float* logits;
+  int T, H, I, E, k;
+  const uint8_t *w13_codes, *w2_codes;
+  const float *w13_scale, *w2_scale;
+  int* counters;
+  float* parts;
+  float* slots;
+  uint8_t* h_codes;
+  float* h_scale;
+  void* out;
+};
+bool fp8_layer_fits(int T, int H, int I, int E, int k);
+Fp8LayerSizes fp8_layer_sizes(int T, int H, int I, int E, int k);
+nvfp4moe_status launch_fp8_layer(const Fp8LayerCall& c, cudaStream_t s);
 
 }  // namespace nvfp4moe

@@ -660,13 +660,15 @@ class FP8MoeFFN:
     """The routed feed-forward layer on FP8 weights (fp8_moe_ffn_forward) with a cached workspace:
     x and the intermediate h are quantised per row and 128 columns inside the call, out is bf16."""
 
-    def __init__(self, experts: FP8Experts, top_k: int):
+    def __init__(self, experts: FP8Experts, top_k: int, launch: int = C.LAUNCH_AUTO):
+        """launch: LAUNCH_AUTO, LAUNCH_SINGLE (the whole layer as one persistent launch, batches of
+        at most 32 tokens) or LAUNCH_MULTI."""
         self.w = experts
         self.top_k = top_k
         self._ws = {}    # size class (bytes) -> buffer
         self._need = {}  # T -> workspace bytes
         d = C.Fp8MoeFfnDesc()
-        d.H, d.I, d.E, d.top_k = experts.H, experts.I, experts.E, top_k
+        d.H, d.I, d.E, d.top_k, d.launch_mode = experts.H, experts.I, experts.E, top_k, launch
         d.w13_codes, d.w13_scale = experts.w13_codes.data_ptr(), experts.w13_scale.data_ptr()
         d.w2_codes, d.w2_scale = experts.w2_codes.data_ptr(), experts.w2_scale.data_ptr()
         self._desc = d
