@@ -132,6 +132,7 @@ Layout make_layout(const fp8_moe_ffn_desc& d) {
     const Fp8LayerSizes z = fp8_layer_sizes(d.T, d.H, d.I, d.E, d.top_k);
     L.counters = put(z.counters * 4), L.parts = put(z.parts * 4), L.slots = put(z.slots * 4);
     L.h_codes = put(z.h_codes), L.h_scale = put(z.h_scale * 4);
+    L.x_codes = put(z.x_codes), L.x_scale = put(z.x_scale * 4);
     L.total = at;
     return L;
   }
@@ -186,6 +187,7 @@ nvfp4moe_status fp8_moe_ffn_forward(const fp8_moe_ffn_desc* desc, const void* x,
     c.w13_codes = d.w13_codes, c.w2_codes = d.w2_codes, c.w13_scale = d.w13_scale, c.w2_scale = d.w2_scale;
     c.counters = i32(L.counters), c.parts = f32(L.parts), c.slots = f32(L.slots);
     c.h_codes = ws + L.h_codes, c.h_scale = f32(L.h_scale);
+    c.x_codes = ws + L.x_codes, c.x_scale = f32(L.x_scale);
     return launch_fp8_layer(c, s);
   }
   st = launch_batch_prologue(x, logits, d.T, d.H, d.E, d.top_k, 1, 0, nullptr, i32(L.ids), f32(L.w), i32(L.counts),

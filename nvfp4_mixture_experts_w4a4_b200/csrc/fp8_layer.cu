@@ -1,11 +1,12 @@
-// The whole FP8 routed layer in one persistent launch for batches of at most 32 tokens (after a
-// small launch that zeroes its counters): routing, x in E4M3, gate/up, SwiGLU, h in E4M3, down and
-// the combine in slot order.
+// The whole FP8 routed layer in one persistent launch for batches of at most 32 tokens: routing,
+// gate/up, SwiGLU, h in E4M3, down and the combine in slot order.  A small launch before it puts x
+// in E4M3 and zeroes the counters; the layer's launch is its programmatic dependent and routes
+// meanwhile.
 //
 // Such a batch is a stream of expert weights, 3 H I bytes per touched expert, against a few rows of
 // activations: its time is those bytes over the memory's rate plus what precedes and follows the
 // stream.  One CTA per SM routes the whole batch itself, so the stream starts as soon as the logits
-// have been read, and keeps x in shared memory as the MMA's B operand; the weights are its M side (128
+// have been read, and keeps x in shared memory (by TMA) as the MMA's B operand; the weights are its M side (128
 // rows), the batch its N side (16 or 32 columns).  A stage of the ring is two 128 x 128 tiles of
 // weights (32 KB) with a scale each:
 //   gate/up unit (expert, 128 columns of h): a gate and an up tile per block of H.  Its sums, with
@@ -20,8 +21,10 @@
 // Combine: after a grid-wide barrier every CTA sums a slice of the outputs over the k slots of a
 // token, in slot order, and rounds once.
 //
-// Warps: 0 streams weights (TMA); 1 owns TMEM and issues the MMAs; 2 fetches scales, and h for down
-// stages; 4..7 add and finish the first tile of every stage, 8..11 the second; 3..15 quantise x first.
+// Warps: 0 streams weights (TMA); 1 owns TMEM and issues the MMAs; 2 and 3 fetch x and its scales;
+// 4..7 add and finish the first tile of every stage, 8..11 the second; 12..15 take every fourth stage
+// each and fetch its scales, and h for down stages (four, because each waits out an L2 read a stage:
+// one warp alone ran a stage in 1.0 us where the weights come in 0.75).
 // Every wait is bounded (status bit on timeout; copies in flight land before the CTA exits).
 #include "fp8.cuh"
 #include "fp8_tile.cuh"
@@ -37,7 +40,7 @@ using namespace sm100;
 constexpr int kThreads = 512;
 constexpr int kTile = 128 * 128;         // bytes of a weight tile
 constexpr int kStage = 2 * kTile;
-constexpr int kMaxStages = 6, kMinStages = 3;
+constexpr int kMaxStages = 6, kMinStages = 3;  // (more than 8 or less than 3: see the scale warps)
 constexpr int kSlots = 8;                // accumulator slots (stages in flight past the MMA)
 constexpr int kMaxE = 1024;
 constexpr int kPitch = 132;              // floats of a row of the exchange buffer
@@ -49,8 +52,8 @@ constexpr uint32_t kPolls = 1u << 22;
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 struct LayerArgs {
-  const __nv_bfloat16* x;
   const float* logits;
+  const float* x_scale;    // [T][nH]
   int T, H, I, E, k;
   int nH, nI;              // 128-blocks
   int stages;
@@ -107,27 +110,26 @@ struct Plan {
     A = active, G = grid;
     s1 = 1, s2 = 1;
     const int u1 = A * a.nI, u2 = A * a.nH, st2 = ceil_div(a.nI, 2);
-    // Parts of a unit: the count with the fewest stages in the fullest CTA, a part costing two
-    // stages more than its own.
+    // Parts of a unit: the count with the fewest stages in the fullest CTA, a split gate/up unit
+    // costing six stages for the exchange of its parts and a down unit one for its end.  A lane tries one count.
+    const int s = (threadIdx.x & 31) + 1;
     if (u1 < G) {
-      int least = INT32_MAX;
-      for (int s = 1; s <= kMaxSplit && s <= a.nH && u1 * s <= a.max_parts; ++s) {
-        const int cost = ceil_div(u1 * s, G) * (ceil_div(a.nH, s) + (s > 1 ? 2 : 0));
-        if (cost < least) least = cost, s1 = s;
-      }
+      int cost = INT32_MAX;
+      if (s <= kMaxSplit && s <= a.nH && u1 * s <= a.max_parts)
+        cost = (ceil_div(u1 * s, G) * (ceil_div(a.nH, s) + (s > 1 ? 6 : 0))) * 32 + s - 1;
+      s1 = (__reduce_min_sync(0xffffffffu, cost) & 31) + 1;
     }
     if (u2 < 4 * G) {
-      int least = INT32_MAX;
-      for (int s = 1; s <= a.chunks_cap && s <= st2; ++s) {
-        const int cost = ceil_div(u2 * s, G) * (ceil_div(st2, s) + 1);
-        if (cost < least) least = cost, s2 = s;
-      }
+      int cost = INT32_MAX;
+      if (s <= a.chunks_cap && s <= st2) cost = ceil_div(u2 * s, G) * (ceil_div(st2, s) + 1) * 32 + s - 1;
+      s2 = (__reduce_min_sync(0xffffffffu, cost) & 31) + 1;
     }
     const int U1 = u1 * s1, U2 = u2 * s2;
     heavy = U1 % G;
     light = G - heavy;
     n1 = U1 / G + (cta < heavy ? 1 : 0);
-    extra = heavy > 0 ? min(ceil_div(a.nH, s1) / ceil_div(st2, s2), U2 / light) : 0;
+    // (with one round of gate/up units no h is ready earlier for the CTAs that have none)
+    extra = heavy > 0 && U1 > G ? min(ceil_div(a.nH, s1) / ceil_div(st2, s2), U2 / light) : 0;
     const int rest = U2 - extra * light;
     first2 = (cta + G - heavy) % G;  // place among the CTAs that share the rest: light ones first
     n2 = (cta >= heavy ? extra : 0) + rest / G + (first2 < rest % G ? 1 : 0);
@@ -194,8 +196,18 @@ __device__ __forceinline__ int load_acquire(const int* p) {
   asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
+// One more at *p, releasing what this thread and those it has met at a barrier wrote before.
 __device__ __forceinline__ void add_release(int* p) {
   asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(p) : "memory");
+}
+// The same, returning the count before and acquiring what the others released.
+__device__ __forceinline__ int add_acq_rel(int* p) {
+  int v;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 // Waits until *p >= want; false when it gave up.
 __device__ __forceinline__ bool wait_count(const int* p, int want) {
@@ -223,15 +235,53 @@ __device__ __forceinline__ void read_columns(uint32_t taddr, uint32_t (&r)[NT]) 
   tmem_ld_wait();
 }
 
-__global__ void fp8_layer_reset_kernel(int* counters, int n) {
+// x [T][H] bf16 -> E4M3 and scales (eight lanes a group of 128), and the layer's counters to zero.
+__global__ void __launch_bounds__(256)
+fp8_layer_prepare_kernel(const __nv_bfloat16* __restrict__ x, int T, int H, uint8_t* __restrict__ codes,
+                         float* __restrict__ scale, int* __restrict__ counters, int n) {
   griddep_launch_dependents();
-  for (int i = threadIdx.x; i < n; i += blockDim.x) counters[i] = 0;
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) counters[i] = 0;
+  const int nH = ceil_div(H, 128), sub = threadIdx.x & 7;
+  const int g = (blockIdx.x * 256 + threadIdx.x) >> 3;
+  const int t = g / nH, kb = g - t * nH;
+  uint32_t u[2][4], mx = 0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int c = kb * 128 + (sub + 8 * j) * 8;
+    uint4 q = make_uint4(0u, 0u, 0u, 0u);
+    if (t < T && c < H) q = __ldg(reinterpret_cast<const uint4*>(x + int64_t(t) * H + c));
+    u[j][0] = q.x, u[j][1] = q.y, u[j][2] = q.z, u[j][3] = q.w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx = __vmaxu2(mx, u[j][i] & 0x7FFF7FFFu);
+  }
+  mx = max(mx << 16, mx & 0xFFFF0000u);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const Fp8ScaleBf16 f = fp8_scale_bf16(mx);
+  if (t >= T) return;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int c = kb * 128 + (sub + 8 * j) * 8;
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float v[4];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        v[2 * q] = __uint_as_float(u[j][2 * i + q] << 16);
+        v[2 * q + 1] = __uint_as_float(u[j][2 * i + q] & 0xFFFF0000u);
+      }
+      w[i] = fp8_encode4(v, f);
+    }
+    if (c < H) *reinterpret_cast<uint2*>(codes + int64_t(t) * H + c) = make_uint2(w[0], w[1]);
+  }
+  if (sub == 0) scale[t * nH + kb] = f.scale;
 }
 
 template <int NT, int PER_LANE>
 __global__ void __launch_bounds__(kThreads, 1)
 fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant__ CUtensorMap tm2,
-                 const __grid_constant__ CUtensorMap tmh, const LayerArgs a) {
+                 const __grid_constant__ CUtensorMap tmh, const __grid_constant__ CUtensorMap tmx, const LayerArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_shared_1024(smem_raw);
   const Smem m = smem_layout(NT, a.nH, a.k, a.E, a.stages);
@@ -256,7 +306,12 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
   __shared__ int s_active, s_scan[2][kThreads / 32], s_last;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
-  constexpr int XWARPS = kThreads / 32 - 3;
+  // Scale warps: stage it is warp 12 + it % W's.  A wait on a barrier's parity is only meant for the
+  // phase before it or the one before that, so a warp that skips stages has to know that the barrier
+  // is not two phases back.  It waits for `empty` first: at its last visit, W stages ago, stage
+  // it - W - S was consumed, which is it - 2S or later as W <= S.  Then stage it - S is consumed, so
+  // the accumulators of it - S - 8 have been read, which is it - 16 or later as S <= 8.
+  const int W = a.stages >= 4 ? 4 : 3;
 
   // ---- set-up, with the logits on their way ----
   constexpr int TOK = NT / 16;  // tokens a warp routes
@@ -279,7 +334,7 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
       mbar_init(&acc_full[s], 1);
       mbar_init(&acc_empty[s], 8);
     }
-    mbar_init(x_full, XWARPS * 32);
+    mbar_init(x_full, 33);
     mbar_init(drain, 1);
     abort_flag = 0;
     mbar_fence_init();
@@ -292,6 +347,7 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
     prefetch_tensormap(&tm13);
     prefetch_tensormap(&tm2);
     prefetch_tensormap(&tmh);
+    prefetch_tensormap(&tmx);
   }
   for (int e = threadIdx.x; e < a.E; e += kThreads) s_mask[e] = 0u;
   __syncthreads();
@@ -331,7 +387,9 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
     if (lane == 31) s_scan[0][warp] = ia, s_scan[1][warp] = ir;
     __syncthreads();
     ia -= act, ir -= rows;
-    for (int w = 0; w < warp; ++w) ia += s_scan[0][w], ir += s_scan[1][w];
+    const bool before = lane < warp;  // the warps before this one (there are 16)
+    ia += __reduce_add_sync(0xffffffffu, before ? s_scan[0][lane & 15] : 0);
+    ir += __reduce_add_sync(0xffffffffu, before ? s_scan[1][lane & 15] : 0);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int e = 2 * int(threadIdx.x) + i;
@@ -358,56 +416,6 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
     abort_flag = 1;
     atomicOr(a.status, kTimeout);
   };
-
-  // ---- x in E4M3, in the MMA's layout: eight lanes a group of 128 ----
-  if (warp >= 3) {
-    const int sub = lane & 7;
-    const int groups = a.T * a.nH;
-    for (int g0 = (warp - 3) * 4; g0 < groups; g0 += XWARPS * 4) {
-      const int g = g0 + (lane >> 3);
-      const int t = g / a.nH, kb = g - t * a.nH;
-      uint32_t u[2][4];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int c = kb * 128 + (sub + 8 * j) * 8;
-        uint4 q = make_uint4(0u, 0u, 0u, 0u);
-        if (g < groups && c < a.H) q = __ldg(reinterpret_cast<const uint4*>(a.x + int64_t(t) * a.H + c));
-        u[j][0] = q.x, u[j][1] = q.y, u[j][2] = q.z, u[j][3] = q.w;
-      }
-      uint32_t mx = 0;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mx = __vmaxu2(mx, u[j][i] & 0x7FFF7FFFu);
-      mx = max(mx << 16, mx & 0xFFFF0000u);
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const Fp8ScaleBf16 f = fp8_scale_bf16(mx);
-      if (g < groups) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          uint32_t w[2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float v[4];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              v[2 * q] = __uint_as_float(u[j][2 * i + q] << 16);
-              v[2 * q + 1] = __uint_as_float(u[j][2 * i + q] & 0xFFFF0000u);
-            }
-            w[i] = fp8_encode4(v, f);
-          }
-          // 128-byte rows, 16-byte pieces exchanged by the row's low three bits
-          const int piece = (sub + 8 * j) >> 1;
-          uint8_t* dst = smem + m.x + kb * NT * 128 + t * 128 + ((piece ^ (t & 7)) << 4) + (sub & 1) * 8;
-          *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-        }
-        if (sub == 0) s_xs[kb * NT + t] = f.scale;
-      }
-    }
-    fence_proxy_async_shared();
-    mbar_arrive(x_full);
-  }
 
   if (warp == 0) {
     if (elect_one()) {
@@ -470,61 +478,72 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
       mbar_wait(drain, 0, 1u << 20);
     }
   } else if (warp == 2) {
+    griddep_wait();  // x comes from the launch before
+    if (elect_one()) {
+      mbar_arrive_expect_tx(x_full, a.nH * NT * 128);
+      for (int kb = 0; kb < a.nH; ++kb) load_tile(smem + m.x + kb * NT * 128, &tmx, kb * 128, 0, 0, x_full);
+    }
+  } else if (warp == 3) {
+    griddep_wait();
+    for (int i = lane; i < a.nH * a.T; i += 32) {
+      const int t = i / a.nH, kb = i - t * a.nH;
+      s_xs[kb * NT + t] = __ldg(a.x_scale + i);
+    }
+    mbar_arrive(x_full);
+  } else if (warp >= 12) {
     // scales of the stage's two tiles, and for down stages h and its scales
     uint32_t it = 0;
-    bool waited = false;  // for the launch that zeroed the counters
-    int have = -1;        // the expert whose h is known to be complete
-    for (int i = 0; i < units && !abort_flag; ++i) {
+    int have = -1;  // the expert whose h is known to be complete
+    bool ok = true;
+    griddep_wait();  // the counters are zero
+    for (int i = 0; i < units && ok && !abort_flag; ++i) {
       const Unit u = unit_of(p, a, i, cta);
       const int e = s_list[u.a], row0 = s_row0[u.a], n = s_row0[u.a + 1] - row0;
-      if (u.down && u.a != have) {
-        if (!waited) griddep_wait(), waited = true;
-        if (!wait_count(a.done + u.a, a.nI)) {
-          abort_now();
-          break;
-        }
-        have = u.a;
-        asm volatile("fence.proxy.async;" ::: "memory");  // h was written by ordinary stores
-      }
-      bool ok = true;
       for (int j = u.j0; j < u.j1; ++j, ++it) {
+        if (int(it % W) != warp - 12) continue;
         const int s = it % S, slot = it % kSlots;
-        float sb = 0.0f, hs[2] = {0.0f, 0.0f};
+        float sb = 0.0f;
         if (u.down) {
           if (lane < 2 && 2 * j + lane < a.nI) sb = __ldg(a.w2_scale + (int64_t(e) * a.nH + u.blk) * a.nI + 2 * j + lane);
+          if (u.a != have) {
+            if (!wait_count(a.done + u.a, a.nI)) {
+              abort_now();
+              ok = false;
+              break;
+            }
+            have = u.a;
+            asm volatile("fence.proxy.async;" ::: "memory");  // h was written by ordinary stores
+          }
+        } else if (lane < 2) {
+          sb = __ldg(a.w13_scale + ((int64_t(e) * 2 + lane) * a.nI + u.blk) * a.nH + j);
+        }
+        if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1) || !mbar_wait(&acc_empty[slot], ((it / kSlots) & 1) ^ 1)) {
+          abort_now();
+          ok = false;
+          break;
+        }
+        if (u.down) {
+          if (lane == 0) {
+            mbar_expect_tx(&full[s], 2 * NT * 128);
+            load_tile(smem + m.h + 2 * s * NT * 128, &tmh, 2 * j * 128, row0, 0, &full[s]);
+            load_tile(smem + m.h + (2 * s + 1) * NT * 128, &tmh, (2 * j + 1) * 128, row0, 0, &full[s]);
+          }
+          float hs[2] = {0.0f, 0.0f};
           if (lane < n) {
             const float* q = a.h_scale + int64_t(row0 + lane) * a.nI + 2 * j;
             hs[0] = __ldcg(q);
             if (2 * j + 1 < a.nI) hs[1] = __ldcg(q + 1);
           }
-        } else if (lane < 2) {
-          sb = __ldg(a.w13_scale + ((int64_t(e) * 2 + lane) * a.nI + u.blk) * a.nH + j);
-        }
-        if (!mbar_wait(&acc_empty[slot], ((it / kSlots) & 1) ^ 1) || !mbar_wait(&empty[s], ((it / S) & 1) ^ 1)) {
-          abort_now();
-          ok = false;
-          break;
-        }
-        if (lane < 2) s_sb[2 * slot + lane] = sb;
-        if (u.down && lane < NT) {
-          s_hs[(2 * slot) * NT + lane] = hs[0];
-          s_hs[(2 * slot + 1) * NT + lane] = hs[1];
-        }
-        __syncwarp();
-        if (lane == 0) {
-          if (u.down) {
-            mbar_arrive_expect_tx(&full[s], 2 * NT * 128);
-            load_tile(smem + m.h + 2 * s * NT * 128, &tmh, 2 * j * 128, row0, 0, &full[s]);
-            load_tile(smem + m.h + (2 * s + 1) * NT * 128, &tmh, (2 * j + 1) * 128, row0, 0, &full[s]);
-          } else {
-            mbar_arrive(&full[s]);
+          if (lane < NT) {
+            s_hs[(2 * slot) * NT + lane] = hs[0];
+            s_hs[(2 * slot + 1) * NT + lane] = hs[1];
           }
         }
+        if (lane < 2) s_sb[2 * slot + lane] = sb;
         __syncwarp();
+        if (lane == 0) mbar_arrive(&full[s]);
       }
-      if (!ok) break;
     }
-    if (!waited) griddep_wait();
   } else if (warp >= 4 && warp < 12) {
     const int half = (warp - 4) >> 2, q = warp & 3, r = q * 32 + lane;
     const uint32_t trow = tmem + (uint32_t(q * 32) << 16);
@@ -587,13 +606,8 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
 #pragma unroll
           for (int c = 0; c < NT; ++c)
             if (c < a.T) __stcg(dst + c * 128, acc[c]);
-          __threadfence();
           add_barrier();
-          if (threadIdx.x == 128) {
-            const int before = atomicAdd(a.tickets + u.id, 1);
-            __threadfence();
-            s_last = before == p.s1 - 1;
-          }
+          if (threadIdx.x == 128) s_last = add_acq_rel(a.tickets + u.id) == p.s1 - 1;
           add_barrier();
           finish = s_last != 0;
           if (finish) {
@@ -633,14 +647,12 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
             if (i0 < a.I) *reinterpret_cast<uint32_t*>(a.h_codes + int64_t(row0 + c) * a.I + i0) = codes;
             if (lane == 0) a.h_scale[int64_t(row0 + c) * a.nI + u.blk] = f.scale;
           }
-          __threadfence();
           add_barrier();
           if (threadIdx.x == 128) add_release(a.done + u.a);
         }
       }
     }
     // ---- combine ----
-    __threadfence();
     add_barrier();
     if (threadIdx.x == 128) {
       add_release(a.gbar);
@@ -694,22 +706,22 @@ int chunks_for(int H, int I) {
 constexpr int kMaxParts = 4 * 148;
 
 template <int NT, int PER_LANE>
-cudaError_t launch_one(const CUtensorMap& m13, const CUtensorMap& m2, const CUtensorMap& mh, const LayerArgs& a,
+cudaError_t launch_one(const CUtensorMap& m13, const CUtensorMap& m2, const CUtensorMap& mh, const CUtensorMap& mx, const LayerArgs& a,
                        int grid, size_t smem, cudaStream_t s) {
   constexpr auto kern = fp8_layer_kernel<NT, PER_LANE>;
   const cudaError_t e = set_smem_limit_once<kern>(kSmemLimit);
-  return e != cudaSuccess ? e : launch_cooperative_dependent(kern, dim3(grid), dim3(kThreads), smem, s, m13, m2, mh, a);
+  return e != cudaSuccess ? e : launch_cooperative_dependent(kern, dim3(grid), dim3(kThreads), smem, s, m13, m2, mh, mx, a);
 }
 
 template <int NT>
-cudaError_t launch_columns(const CUtensorMap& m13, const CUtensorMap& m2, const CUtensorMap& mh, const LayerArgs& a,
+cudaError_t launch_columns(const CUtensorMap& m13, const CUtensorMap& m2, const CUtensorMap& mh, const CUtensorMap& mx, const LayerArgs& a,
                            int grid, size_t smem, cudaStream_t s) {
   const int per = (a.E + 31) / 32;
-  if (per <= 1) return launch_one<NT, 1>(m13, m2, mh, a, grid, smem, s);
-  if (per <= 4) return launch_one<NT, 4>(m13, m2, mh, a, grid, smem, s);
-  if (per <= 8) return launch_one<NT, 8>(m13, m2, mh, a, grid, smem, s);
-  if (per <= 16) return launch_one<NT, 16>(m13, m2, mh, a, grid, smem, s);
-  return launch_one<NT, 32>(m13, m2, mh, a, grid, smem, s);
+  if (per <= 1) return launch_one<NT, 1>(m13, m2, mh, mx, a, grid, smem, s);
+  if (per <= 4) return launch_one<NT, 4>(m13, m2, mh, mx, a, grid, smem, s);
+  if (per <= 8) return launch_one<NT, 8>(m13, m2, mh, mx, a, grid, smem, s);
+  if (per <= 16) return launch_one<NT, 16>(m13, m2, mh, mx, a, grid, smem, s);
+  return launch_one<NT, 32>(m13, m2, mh, mx, a, grid, smem, s);
 }
 
 }  // namespace
@@ -727,13 +739,15 @@ Fp8LayerSizes fp8_layer_sizes(int T, int H, int I, int E, int k) {
   z.slots = P * chunks_for(H, I) * H;
   z.h_codes = P * I;
   z.h_scale = P * nI;
+  z.x_codes = int64_t(T) * H;
+  z.x_scale = T * fp8_blocks(H);
   return z;
 }
 
 nvfp4moe_status launch_fp8_layer(const Fp8LayerCall& c, cudaStream_t s) {
   LayerArgs a{};
-  a.x = static_cast<const __nv_bfloat16*>(c.x);
   a.logits = c.logits;
+  a.x_scale = c.x_scale;
   a.T = c.T, a.H = c.H, a.I = c.I, a.E = c.E, a.k = c.k;
   a.nH = int(fp8_blocks(c.H)), a.nI = int(fp8_blocks(c.I));
   a.stages = stages_for(c.T, c.H, c.E, c.k);
@@ -747,15 +761,17 @@ nvfp4moe_status launch_fp8_layer(const Fp8LayerCall& c, cudaStream_t s) {
   a.status = device_status_ptr();
   if (!a.status) return fail(NVFP4MOE_CUDA_ERROR, "device status word unavailable");
   const int nt = columns_for(c.T);
-  CUtensorMap m13, m2, mh;
+  CUtensorMap m13, m2, mh, mx;
   nvfp4moe_status st = make_fp8_map(&m13, c.w13_codes, c.H, c.I, 2 * int64_t(c.E), c.H, int64_t(c.I) * c.H, 128);
   if (st == NVFP4MOE_OK) st = make_fp8_map(&m2, c.w2_codes, c.I, c.H, c.E, c.I, int64_t(c.I) * c.H, 128);
   if (st == NVFP4MOE_OK) st = make_fp8_map(&mh, c.h_codes, c.I, int64_t(c.T) * c.k, 1, c.I, c.I, nt);
+  if (st == NVFP4MOE_OK) st = make_fp8_map(&mx, c.x_codes, c.H, c.T, 1, c.H, c.H, nt);
   if (st != NVFP4MOE_OK) return st;
-  fp8_layer_reset_kernel<<<1, 512, 0, s>>>(c.counters, touched + kMaxParts + 1);
+  fp8_layer_prepare_kernel<<<(c.T * a.nH * 8 + 255) / 256, 256, 0, s>>>(
+      static_cast<const __nv_bfloat16*>(c.x), c.T, c.H, c.x_codes, c.x_scale, c.counters, touched + kMaxParts + 1);
   const size_t smem = smem_layout(nt, a.nH, c.k, c.E, a.stages).total;
-  const cudaError_t e = nt == 16 ? launch_columns<16>(m13, m2, mh, a, num_sms(), smem, s)
-                                 : launch_columns<32>(m13, m2, mh, a, num_sms(), smem, s);
+  const cudaError_t e = nt == 16 ? launch_columns<16>(m13, m2, mh, mx, a, num_sms(), smem, s)
+                                 : launch_columns<32>(m13, m2, mh, mx, a, num_sms(), smem, s);
   if (e != cudaSuccess) return fail(NVFP4MOE_CUDA_ERROR, "fp8 layer: %s", cudaGetErrorString(e));
   return check_launch("fp8 layer");
 }

@@ -64,7 +64,7 @@ nvfp4moe_status make_fp8_map(CUtensorMap* map, const void* base, int64_t K, int6
 
 // The whole layer in one persistent launch, for batches of at most 32 tokens (fp8_layer.cu).
 struct Fp8LayerSizes {
-  int64_t counters, parts, slots, h_codes, h_scale;  // elements (int, float, float, byte, float)
+  int64_t counters, parts, slots, h_codes, h_scale, x_codes, x_scale;  // elements of their types below
 };
 struct Fp8LayerCall {
   const void* x;
@@ -77,6 +77,8 @@ struct Fp8LayerCall {
   float* slots;
   uint8_t* h_codes;
   float* h_scale;
+  uint8_t* x_codes;
+  float* x_scale;
   void* out;
 };
 bool fp8_layer_fits(int T, int H, int I, int E, int k);
