@@ -499,21 +499,16 @@ def _same_device(*ts):
     return dev
 
 
-class _on:
-    """Makes the device of a call's tensors current for its launches (free when it is already)."""
-
-    def __init__(self, dev):
-        self.dev, self.back = dev.index, None
-
-    def __enter__(self):
-        now = torch.cuda.current_device()
-        if now != self.dev:
-            self.back = now
-            torch.cuda.set_device(self.dev)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
+def _call(dev, fn: str, *args):
+    """Calls the library with `dev` current and its current stream as the last argument."""
+    now = torch.cuda.current_device()
+    if now == dev.index:
+        st = getattr(lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(now))
+    else:
+        with torch.cuda.device(dev):
+            st = getattr(lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if st != C.OK:
+        check(st, fn)
 
 
 def _fp8_codes(t: torch.Tensor, what: str):
@@ -542,13 +537,14 @@ def fp8_quantize(x: torch.Tensor, *, tile: int = FP8_ROWS, codes: torch.Tensor |
     dev = _same_device(x, codes, scale)
     shape = x.shape
     rows, K = shape[-2], shape[-1]
-    B = shape[0] if x.dim() == 3 else 1
-    if K > 1 and x.stride(-1) != 1:
+    stride = x.stride()
+    if K > 1 and stride[-1] != 1:
         raise ValueError("x must have unit stride along K")
-    srows = rows if tile == FP8_ROWS else _fp8_blocks(rows)
+    nk = (K + 127) // 128
+    srows = rows if tile == FP8_ROWS else (rows + 127) // 128
     if codes is None:
         pitch = (K + 15) // 16 * 16
-        codes = torch.empty(*shape[:-1], pitch, dtype=torch.float8_e4m3fn, device=dev)
+        codes = torch.empty((*shape[:-1], pitch), dtype=torch.float8_e4m3fn, device=dev)
         if pitch != K:
             codes = codes[..., :K]
     else:
@@ -556,17 +552,17 @@ def fp8_quantize(x: torch.Tensor, *, tile: int = FP8_ROWS, codes: torch.Tensor |
         if codes.shape != shape or (K > 1 and codes.stride(-1) != 1):
             raise ValueError(f"codes must be {tuple(shape)} with unit stride along K")
     if scale is None:
-        scale = torch.empty(*shape[:-2], srows, _fp8_blocks(K), dtype=torch.float32, device=dev)
-    elif (scale.dtype != torch.float32 or scale.shape != (*shape[:-2], srows, _fp8_blocks(K))
-          or (scale.shape[-1] > 1 and scale.stride(-1) != 1)):
-        raise ValueError(f"scale must be fp32 {(*shape[:-2], srows, _fp8_blocks(K))} with unit stride along K")
-    batched = x.dim() == 3
-    with _on(dev):
-        st = lib().fp8_quantize(x.data_ptr(), dt, B, rows, K, x.stride(-2), x.stride(0) if batched else 0, tile,
-                                codes.data_ptr(), codes.stride(-2), codes.stride(0) if batched else 0,
-                                scale.data_ptr(), scale.stride(-2), scale.stride(0) if batched else 0,
-                                torch.cuda.current_stream().cuda_stream)
-    check(st, "fp8_quantize")
+        scale = torch.empty((*shape[:-2], srows, nk), dtype=torch.float32, device=dev)
+    elif (scale.dtype != torch.float32 or scale.shape != (*shape[:-2], srows, nk)
+          or (nk > 1 and scale.stride(-1) != 1)):
+        raise ValueError(f"scale must be fp32 {(*shape[:-2], srows, nk)} with unit stride along K")
+    cs, ss = codes.stride(), scale.stride()
+    if x.dim() == 3:
+        B, xb, cb, sb = shape[0], stride[0], cs[0], ss[0]
+    else:
+        B, xb, cb, sb = 1, 0, 0, 0
+    _call(dev, "fp8_quantize", x.data_ptr(), dt, B, rows, K, stride[-2], xb, tile, codes.data_ptr(), cs[-2], cb,
+          scale.data_ptr(), ss[-2], sb)
     return codes, scale
 
 
@@ -595,21 +591,21 @@ def fp8_gemm(A: torch.Tensor, A_scale: torch.Tensor, B: torch.Tensor, B_scale: t
         raise ValueError("D is bf16 or fp32")
     dev = _same_device(A, A_scale, B, B_scale, out)
     if out is None:
-        out = torch.empty(M, N, dtype=out_dtype, device=dev)
-    if (K > 1 and (A.stride(1) != 1 or B.stride(1) != 1)) or (N > 1 and out.stride(1) != 1) or \
-            (nk > 1 and (A_scale.stride(1) != 1 or B_scale.stride(1) != 1)):
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    (lda, ka), (ldb, kb), (lds_a, na), (lds_b, nb), (ldd, no) = (
+        A.stride(), B.stride(), A_scale.stride(), B_scale.stride(), out.stride())
+    if (K > 1 and (ka != 1 or kb != 1)) or (N > 1 and no != 1) or (nk > 1 and (na != 1 or nb != 1)):
         raise ValueError("every tensor must have unit stride along its last axis")
-
-    def pitch(t, n):  # a single row has no pitch: any that the kernels accept
-        return t.stride(0) if t.shape[0] > 1 else n
-
+    # a single row has no pitch: any that the kernels accept
     wide = (K + 15) // 16 * 16
-    with _on(dev):
-        st = lib().fp8_gemm(A.data_ptr(), pitch(A, wide), A_scale.data_ptr(), pitch(A_scale, nk), B.data_ptr(),
-                            pitch(B, wide), B_scale.data_ptr(), pitch(B_scale, nk), M, N, K, out.data_ptr(),
-                            pitch(out, N), C.DTYPE_F32 if out_dtype == torch.float32 else C.DTYPE_BF16,
-                            torch.cuda.current_stream().cuda_stream)
-    check(st, "fp8_gemm")
+    if M == 1:
+        lda, lds_a, ldd = wide, nk, N
+    if N == 1:
+        ldb = wide
+    if N <= 128:
+        lds_b = nk
+    _call(dev, "fp8_gemm", A.data_ptr(), lda, A_scale.data_ptr(), lds_a, B.data_ptr(), ldb, B_scale.data_ptr(), lds_b,
+          M, N, K, out.data_ptr(), ldd, C.DTYPE_F32 if out_dtype == torch.float32 else C.DTYPE_BF16)
     return out
 
 
@@ -673,6 +669,7 @@ class FP8MoeFFN:
         d.w2_codes, d.w2_scale = experts.w2_codes.data_ptr(), experts.w2_scale.data_ptr()
         self._desc = d
         self._descs = {}  # T -> descriptor
+        self._refs = {}   # T -> (reference to the descriptor, workspace)
 
     def desc(self, T: int) -> C.Fp8MoeFfnDesc:
         if T not in self._descs:
@@ -706,16 +703,15 @@ class FP8MoeFFN:
                                 or not out.is_contiguous()):
             raise ValueError(f"out must be a contiguous bf16 [{T}, {w.H}] tensor")
         dev = _same_device(x, logits, out, w.w13_codes)
-        with _on(dev):
-            x = x.contiguous()
-            logits = logits.to(torch.float32).contiguous()
-            if out is None:
-                out = torch.empty(T, w.H, dtype=torch.bfloat16, device=dev)
-            ws = self.workspace(T)
-            st = lib().fp8_moe_ffn_forward(ctypes.byref(self.desc(T)), x.data_ptr(), logits.data_ptr(),
-                                           out.data_ptr(), ws.data_ptr(), ws.numel(),
-                                           torch.cuda.current_stream().cuda_stream)
-        check(st, "fp8_moe_ffn_forward")
+        x = x.contiguous()
+        logits = logits.to(torch.float32).contiguous()
+        if out is None:
+            out = torch.empty((T, w.H), dtype=torch.bfloat16, device=dev)
+        if T not in self._refs:
+            self._refs[T] = (ctypes.byref(self.desc(T)), self.workspace(T))
+        ref, ws = self._refs[T]
+        _call(dev, "fp8_moe_ffn_forward", ref, x.data_ptr(), logits.data_ptr(), out.data_ptr(), ws.data_ptr(),
+              ws.numel())
         return out
 
     __call__ = forward
