@@ -7,7 +7,7 @@
 // accumulators in TMEM); between blocks the partial sum is multiplied by its two scales and added
 // to fp32 registers.  The rows of A are the MMA's M side, so a thread of the adding warps holds one
 // row: both scales are one number a thread, and the multiply-add is one packed FMA for two columns.
-// Two TMEM accumulators of BN columns alternate, so the MMA of block kb + 1 runs under the
+// All of TMEM is accumulators (512 / BN of them), so the MMA of block kb + 1 runs under the
 // additions of block kb.  Per block an SM multiplies for 512 cycles (128 x 256 x 128 at 8192 MACs a
 // cycle) while its eight adding warps read 128 KB of TMEM (256 cycles) and issue 64 packed FMAs a
 // thread (256 cycles a scheduler).
@@ -40,6 +40,7 @@ constexpr int TK = FP8_BLOCK;        // K per stage: one scale block, one 128-by
 constexpr int TTHREADS = 384;
 constexpr int ADD_WARPS = 8;
 constexpr int A_STAGE = TM * TK;
+constexpr int kMaxSplit = 8;         // CTAs of a cluster (the portable size)
 constexpr uint32_t kTimeout = NVFP4MOE_DEV_TIMEOUT;
 
 enum Mode { DENSE = 0, GATEUP = 1, DOWN = 2 };
@@ -52,7 +53,7 @@ constexpr int b_rows(int bn, bool pair) { return pair ? bn / 2 : bn; }
 constexpr int stages_of(int bn, bool pair) { return b_rows(bn, pair) == 256 ? 4 : 6; }
 constexpr int ring_bytes(int bn, bool pair) { return stages_of(bn, pair) * (A_STAGE + b_rows(bn, pair) * TK); }
 constexpr int smem_bytes(int bn, bool pair) {
-  return 1024 + ring_bytes(bn, pair) + (2 * stages_of(bn, pair) + 9) * 8 + 16 + 2 * 2 * TM * 4 + 2 * SC_FLOATS * 4;
+  return 1024 + ring_bytes(bn, pair) + (2 * stages_of(bn, pair) + 2 * (512 / bn) + 5) * 8 + 16 + 2 * 2 * TM * 4 + 2 * SC_FLOATS * 4;
 }
 constexpr int split_pitch(int bn) { return bn + 4; }  // floats; rows 16 bytes apart in the banks
 
@@ -230,6 +231,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   constexpr int B_STAGE = B_ROWS * TK;
   static_assert(!PAIR || (BN == 256 && !SPLIT), "a pair runs 256 x 256 tiles, whole sums");
   constexpr int HALF = BN / 2;          // columns an adding warp holds
+  constexpr uint32_t NACC = 512 / BN;   // accumulators: all of TMEM
   constexpr bool GROUPED = MODE != DENSE;
   static_assert(MODE != GATEUP || BN == 256, "a gate/up tile is one 128-column block of each");
   extern __shared__ uint8_t smem_raw[];
@@ -238,9 +240,9 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   uint8_t* sB = sA + STAGES * A_STAGE;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring_bytes(BN, PAIR));
   uint64_t* empty = full + STAGES;
-  uint64_t* acc_full = empty + STAGES;  // [2]
-  uint64_t* acc_empty = acc_full + 2;   // [2]
-  uint64_t* sc_full = acc_empty + 2;    // [2]
+  uint64_t* acc_full = empty + STAGES;  // [NACC]
+  uint64_t* acc_empty = acc_full + NACC;
+  uint64_t* sc_full = acc_empty + NACC; // [2]
   uint64_t* sc_empty = sc_full + 2;     // [2]
   uint64_t* drain = sc_empty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
@@ -254,7 +256,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < NACC; ++b) {
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], PAIR ? 2 * ADD_WARPS : ADD_WARPS);
     }
@@ -266,7 +268,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     *abort_flag = 0;
     mbar_fence_init();
   }
-  if (warp == 1) alloc_tmem<PAIR>(tmem_holder, 2 * BN);
+  if (warp == 1) alloc_tmem<PAIR>(tmem_holder, 512);
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tmA);
     prefetch_tensormap(&tmB);
@@ -335,8 +337,8 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       for (int t = t_first; t < n_tiles && ok && !*abort_flag; t += t_step) {
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
           const int s = it % STAGES;
-          const uint32_t ab = it & 1;
-          if (!mbar_wait(&acc_empty[ab], ((it >> 1) & 1) ^ 1) || !mbar_wait(&full[s], (it / STAGES) & 1)) {
+          const uint32_t ab = it % NACC;
+          if (!mbar_wait(&acc_empty[ab], ((it / NACC) & 1) ^ 1) || !mbar_wait(&full[s], (it / STAGES) & 1)) {
             abort_now();
             ok = false;
             break;
@@ -417,9 +419,9 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
       for (int i = 0; i < HALF; ++i) acc[i] = 0.0f;
       bool ok = true;
-      auto sums_ready = [&](uint32_t i) { return mbar_try_wait(&acc_full[i & 1], (i >> 1) & 1); };
+      auto sums_ready = [&](uint32_t i) { return mbar_try_wait(&acc_full[i % NACC], (i / NACC) & 1); };
       auto wait_sums = [&](uint32_t i) {
-        if (!mbar_wait(&acc_full[i & 1], (i >> 1) & 1)) {
+        if (!mbar_wait(&acc_full[i % NACC], (i / NACC) & 1)) {
           abort_now();
           ok = false;
         }
@@ -428,8 +430,8 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       auto release_sums = [&](uint32_t i) {
         tc_fence_before();
         if (lane == 0) {
-          if constexpr (PAIR) arrive_at(release_bar + 8 * (i & 1));
-          else arrive_here(&acc_empty[i & 1]);
+          if constexpr (PAIR) arrive_at(release_bar + 8 * (i % NACC));
+          else arrive_here(&acc_empty[i % NACC]);
         }
       };
       // Chunks of 32 columns, each read and added before the next is read: the two warps of a
@@ -457,7 +459,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
             for (int c = 0; c < HALF; c += 32) {
               uint32_t v[32];
-              tmem_ld_32x32b_x32(trow + (it & 1) * BN + column(c), v);
+              tmem_ld_32x32b_x32(trow + (it % NACC) * BN + column(c), v);
               tmem_ld_wait_for(v);
               if (c + 32 == HALF) {
                 release_sums(it);
@@ -526,25 +528,50 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
           }
         }
       } else {
-        if (r < w.rows) {
-          const int n = w.n0 + half * HALF;
+        const int n = w.n0 + half * HALF;
+        if (!p.d_vec) {
+          // Rows that do not start at multiples of 32 bytes: 32 x 32 blocks are transposed through
+          // shuffles, and a store is 32 consecutive columns of one row.
+          if (live) {
+#pragma unroll
+            for (int c = 0; c < HALF; c += 32) {
+              float* v = acc + c;
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if ((i & o) == 0) {
+                    const bool upper = (lane & o) != 0;
+                    const float got = __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + o], o);
+                    if (upper) v[i] = got;
+                    else v[i + o] = got;
+                  }
+              const int col = n + c + lane;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                if (q * 32 + i < w.rows && col < p.N) {
+                  const int64_t to = int64_t(w.row + q * 32 + i) * p.ldd + col;
+                  if (p.d_f32) static_cast<float*>(p.D)[to] = v[i];
+                  else static_cast<__nv_bfloat16*>(p.D)[to] = __float2bfloat16_rn(v[i]);
+                }
+              }
+            }
+          }
+        } else if (r < w.rows) {
           const int64_t at = int64_t(w.row + r) * p.ldd + n;
           if (p.d_f32) {
             float* d = static_cast<float*>(p.D) + at;
 #pragma unroll
             for (int c = 0; c < HALF; c += 8) {
-              float f[8];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) f[2 * i] = acc[c + 2 * i], f[2 * i + 1] = acc[c + 2 * i + 1];
-              if (p.d_vec && n + c + 8 <= p.N) {
+              if (n + c + 8 <= p.N) {
                 uint32_t o[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(f[i]);
+                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(acc[c + i]);
                 store_32b(d + c, o);
               } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                  if (n + c + i < p.N) d[c + i] = f[i];
+                  if (n + c + i < p.N) d[c + i] = acc[c + i];
               }
             }
           } else {
@@ -553,12 +580,8 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             for (int c = 0; c < HALF; c += 16) {
               uint32_t o[8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                float lo, hi;
-                lo = acc[c + 2 * i], hi = acc[c + 2 * i + 1];
-                o[i] = bf16x2(lo, hi);
-              }
-              if (p.d_vec && n + c + 16 <= p.N) {
+              for (int i = 0; i < 8; ++i) o[i] = bf16x2(acc[c + 2 * i], acc[c + 2 * i + 1]);
+              if (n + c + 16 <= p.N) {
                 store_32b(d + c, o);
               } else {
 #pragma unroll
@@ -577,20 +600,19 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   // a pair leaves together: each CTA's shared memory and barriers are used by the other
   if constexpr (PAIR) cluster_barrier();
   tc_fence_after();
-  if (warp == 1) free_tmem<PAIR>(tmem, 2 * BN);
+  if (warp == 1) free_tmem<PAIR>(tmem, 512);
 
   if constexpr (SPLIT) {
     // Every CTA of the cluster runs one tile (the grid is tiles * ranks), reaches both barriers on
-    // every path, and sums columns [rank * BN / ranks, +BN / ranks) over the ranks in order.
+    // every path, and sums its share of the tile's columns over the ranks in order.
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
     const Tile w = tile_of<PAIR>(p, t_first, BN, GROUPED);
-    const int width = BN / ranks, c0 = rank * width;  // a multiple of 16: ranks is at most 8
-    const int per_row = width / 4;
+    const int f0 = BN / 4 * rank / ranks, per_row = BN / 4 * (rank + 1) / ranks - f0;  // groups of four columns
     float* mine = reinterpret_cast<float*>(smem);
     for (int i = threadIdx.x; i < w.rows * per_row; i += TTHREADS) {
-      const int r = i / per_row, c = c0 + (i - r * per_row) * 4;
+      const int r = i / per_row, c = (f0 + i - r * per_row) * 4;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int k = 0; k < ranks; ++k) {
         const float4 x = *reinterpret_cast<const float4*>(cluster.map_shared_rank(mine, k) + r * split_pitch(BN) + c);
@@ -672,29 +694,68 @@ nvfp4moe_status make_fp8_map(CUtensorMap* map, const void* base, int64_t K, int6
   return NVFP4MOE_OK;
 }
 
-// How a dense product is run: the column width of a tile and the K split.  The estimate is rounds
-// of resident CTAs times the blocks a CTA runs, at the cost of one block: a tile of 256 columns
-// takes 1.7 times one of 128 (its B bytes double, its A bytes do not), and a split adds the
-// exchange of the partial tiles, about three blocks' time.
+namespace {
+
+// Clusters of `split` CTAs that run at once, read once per device and variant.
+template <int BN>
+int resident_clusters(int split) {
+  static std::atomic<int> known[64][kMaxSplit + 1];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 0 && dev < 64)
+    if (const int v = known[dev][split].load(std::memory_order_relaxed)) return v;
+  constexpr auto kern = fp8_tile_kernel<DENSE, BN, true, false>;
+  int n = 0;
+  if (set_smem_limit_once<kern>(smem_bytes(BN, false)) == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(num_sms() / split * split));
+    cfg.blockDim = dim3(TTHREADS);
+    cfg.dynamicSmemBytes = smem_bytes(BN, false);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) n = 0;
+  }
+  if (n < 1) {
+    cudaGetLastError();  // the estimate below stands in
+    n = num_sms() / (2 * split);
+  }
+  if (dev >= 0 && dev < 64) known[dev][split].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+}  // namespace
+
+// How a dense product is run: the width of a tile, the CTAs that split its K, and whether pairs of
+// CTAs take 256 rows.  The estimate, in microseconds fitted to measurements on a B200: every round of
+// resident tiles costs its blocks of K (a 128 x 128 tile's in 0.30, a 128 x 256 tile's in 0.62, a
+// pair's in 0.58) and 1.0 for its start and end; a split tile 1.5 + 0.6 a CTA instead, for the
+// exchange.  E.g. 64 x 4096 x 4096: 11.5 measured with 128 columns split over 4, 16.1 unsplit, 27.7
+// over 8 (clusters of 8 do not all fit at once); 2048 x 4096 x 4096: 42.6 in pairs, 46.3 unpaired.
 DensePlan fp8_dense_plan(int64_t M, int64_t N, int64_t K) {
   const int sms = num_sms();
   const int nkb = int(fp8_blocks(K));
-  DensePlan best{256, 1, false};
-  double least = 1e300;
-  for (int bn : {256, 128})
-    for (int split : {1, 2, 4, 8}) {
-      if (split > nkb) continue;
-      const double tiles = double((M + TM - 1) / TM) * double((N + bn - 1) / bn);
-      const double rounds = split == 1 ? double(int64_t((tiles + sms - 1) / sms)) : double(int64_t((tiles * split + sms - 1) / sms));
-      const double cost = rounds * (((nkb + split - 1) / split) * (bn == 256 ? 1.7 : 1.0) + (split > 1 ? 4.0 : 1.0));
-      if (cost < least * 0.999) {
+  auto rounds = [](int64_t tiles, int64_t at_once) { return double((tiles + at_once - 1) / at_once); };
+  const int64_t pairs = ((M + 255) / 256) * ((N + 255) / 256);
+  DensePlan best{256, 1, true};
+  double least = M > TM ? rounds(pairs, sms / 2) * (nkb * 0.58 + 1.0) : 1e300;
+  for (int bn : {256, 128}) {
+    const int64_t tiles = ((M + TM - 1) / TM) * ((N + bn - 1) / bn);
+    for (int split = 1; split <= kMaxSplit; ++split) {
+      if (split > 1 && (split > nkb || tiles * split > sms)) break;
+      const int64_t at_once = split == 1 ? sms : (bn == 256 ? resident_clusters<256>(split) : resident_clusters<128>(split));
+      const double cost = rounds(tiles, at_once) * (((nkb + split - 1) / split) * (bn == 256 ? 0.62 : 0.30) +
+                                                    (split > 1 ? 1.5 + 0.6 * split : 1.0));
+      if (cost < least) {
         least = cost;
         best = DensePlan{bn, split, false};
       }
     }
-  const double pairs = double((M + 255) / 256) * double((N + 255) / 256);
-  const double cost = double(int64_t((pairs * 2 + sms - 1) / sms)) * (nkb * 1.2 + 1.0);
-  if (M > 128 && cost < least) best = DensePlan{256, 1, true};
+  }
   return best;
 }
 
