@@ -1,0 +1,118 @@
+"""Host-side checks of the FP8 entry points (no GPU): argument errors come back as statuses before
+anything is launched, and the binding refuses what the kernels do not take."""
+import ctypes
+
+import pytest
+import torch
+
+from nvfp4_mixture_experts_w4a4_b200 import _lib as C
+from nvfp4_mixture_experts_w4a4_b200 import build, ops
+
+
+@pytest.fixture(scope="module")
+def so():
+    build.build()
+    return C.lib()
+
+
+def quantize(so, x=256, dtype=0, batch=1, rows=4, K=64, ldx=64, xb=0, tile=0, codes=256, ldc=64, cb=0, scale=256,
+             lds=1, sb=0):
+    return so.fp8_quantize(x, dtype, batch, rows, K, ldx, xb, tile, codes, ldc, cb, scale, lds, sb, None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(dtype=2), C.INVALID_ARG), (dict(tile=2), C.INVALID_ARG), (dict(rows=-1), C.INVALID_ARG),
+    (dict(x=None), C.INVALID_ARG), (dict(codes=None), C.INVALID_ARG), (dict(scale=None), C.INVALID_ARG),
+    (dict(ldx=63), C.INVALID_ARG), (dict(ldc=63), C.INVALID_ARG), (dict(K=129, ldx=129, ldc=129, lds=1), C.INVALID_ARG),
+    (dict(xb=-1), C.INVALID_ARG), (dict(x=257), C.INVALID_ARG),
+    (dict(rows=1 << 31), C.UNSUPPORTED_SHAPE), (dict(batch=1 << 16, rows=1 << 16), C.UNSUPPORTED_SHAPE),
+    (dict(K=1 << 30, ldx=1 << 30, ldc=1 << 30, lds=1 << 23), C.UNSUPPORTED_SHAPE),
+    (dict(rows=0), C.OK), (dict(batch=0), C.OK), (dict(K=0), C.OK),
+])
+def test_quantize_statuses(so, change, status):
+    assert quantize(so, **change) == status
+
+
+def gemm(so, A=256, lda=256, sa=256, lds_a=2, B=256, ldb=256, sb=256, lds_b=2, M=8, N=8, K=256, D=256, ldd=8, dt=0):
+    return so.fp8_gemm(A, lda, sa, lds_a, B, ldb, sb, lds_b, M, N, K, D, ldd, dt, None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(dt=2), C.INVALID_ARG), (dict(M=-1), C.INVALID_ARG), (dict(A=None), C.INVALID_ARG),
+    (dict(sb=None), C.INVALID_ARG), (dict(D=None), C.INVALID_ARG), (dict(D=257), C.INVALID_ARG),
+    (dict(lda=240), C.INVALID_ARG), (dict(ldb=240), C.INVALID_ARG), (dict(ldd=7), C.INVALID_ARG),
+    (dict(lds_a=1), C.INVALID_ARG), (dict(lds_b=1), C.INVALID_ARG),
+    (dict(lda=260), C.UNSUPPORTED_SHAPE), (dict(ldb=264), C.UNSUPPORTED_SHAPE), (dict(A=264), C.UNSUPPORTED_SHAPE),
+    (dict(B=264), C.UNSUPPORTED_SHAPE), (dict(K=0), C.UNSUPPORTED_SHAPE),
+    (dict(M=1 << 31, N=1, ldd=1), C.UNSUPPORTED_SHAPE), (dict(lda=1 << 41), C.UNSUPPORTED_SHAPE),
+    (dict(M=0), C.OK), (dict(N=0), C.OK),
+])
+def test_gemm_statuses(so, change, status):
+    assert gemm(so, **change) == status
+
+
+def desc(**change):
+    d = C.Fp8MoeFfnDesc()
+    base = dict(T=16, H=256, I=128, E=8, top_k=2, launch_mode=C.LAUNCH_AUTO, w13_codes=256, w13_scale=256,
+                w2_codes=256, w2_scale=256)
+    for name, value in {**base, **change}.items():
+        setattr(d, name, value)
+    return d
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(T=-1), C.INVALID_ARG), (dict(H=100), C.UNSUPPORTED_SHAPE), (dict(H=0), C.UNSUPPORTED_SHAPE),
+    (dict(I=24), C.UNSUPPORTED_SHAPE), (dict(E=1025), C.UNSUPPORTED_SHAPE), (dict(E=0), C.UNSUPPORTED_SHAPE),
+    (dict(top_k=9), C.UNSUPPORTED_SHAPE), (dict(top_k=0), C.UNSUPPORTED_SHAPE),
+    (dict(E=64, top_k=33), C.UNSUPPORTED_SHAPE), (dict(T=1 << 24), C.UNSUPPORTED_SHAPE),
+    (dict(launch_mode=7), C.INVALID_ARG), (dict(launch_mode=C.LAUNCH_SINGLE, T=33), C.UNSUPPORTED_SHAPE),
+    (dict(launch_mode=C.LAUNCH_SINGLE, H=16384), C.UNSUPPORTED_SHAPE),
+])
+def test_layer_statuses(so, change, status):
+    d = desc(**change)
+    assert so.fp8_moe_ffn_workspace_size(ctypes.byref(d)) == 0
+    assert so.fp8_moe_ffn_forward(ctypes.byref(d), 256, 256, 256, 256, 1 << 40, None) == status
+    assert so.nvfp4moe_last_error()
+
+
+def test_layer_pointers_and_workspace(so):
+    d = desc()
+    need = so.fp8_moe_ffn_workspace_size(ctypes.byref(d))
+    assert need > 0
+    for args in ((None, 256, 256, 256), (256, None, 256, 256), (256, 256, None, 256), (256, 256, 256, None),
+                 (264, 256, 256, 256), (256, 256, 264, 256), (256, 256, 256, 128)):
+        assert so.fp8_moe_ffn_forward(ctypes.byref(d), *args, need, None) == C.INVALID_ARG
+    assert so.fp8_moe_ffn_forward(ctypes.byref(desc(w2_scale=None)), 256, 256, 256, 256, need, None) == C.INVALID_ARG
+    assert so.fp8_moe_ffn_forward(ctypes.byref(d), 256, 256, 256, 256, need - 1, None) == C.WORKSPACE_TOO_SMALL
+    assert so.fp8_moe_ffn_forward(ctypes.byref(desc(T=0)), None, None, None, None, 0, None) == C.OK
+    assert so.fp8_moe_ffn_forward(None, 256, 256, 256, 256, need, None) == C.INVALID_ARG
+
+
+def test_binding_refuses():
+    x = torch.zeros(4, 128)
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.fp8_quantize(x)
+    with pytest.raises(ValueError, match="bf16 or fp32"):
+        ops.fp8_quantize(x.half())
+    with pytest.raises(ValueError, match="rows, K"):
+        ops.fp8_quantize(x[0])
+    a, s = torch.zeros(4, 128, dtype=torch.float8_e4m3fn), torch.ones(4, 1)
+    with pytest.raises(ValueError, match="float8_e4m3fn"):
+        ops.fp8_gemm(x, s, a, s[:1])
+    with pytest.raises(ValueError, match="A must be"):
+        ops.fp8_gemm(a, s, a[:, :64], s[:1])
+    with pytest.raises(ValueError, match="A_scale"):
+        ops.fp8_gemm(a, s[:3], a, s[:1])
+    with pytest.raises(ValueError, match="B_scale"):
+        ops.fp8_gemm(a, s, a, s)
+    with pytest.raises(ValueError, match="bf16 or fp32"):
+        ops.fp8_gemm(a, s, a, s[:1], out_dtype=torch.float16)
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.fp8_gemm(a, s, a, s[:1])
+    w13, w2 = torch.zeros(2, 2, 32, 128, dtype=torch.uint8), torch.zeros(2, 128, 32, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="w2_scale"):
+        ops.FP8Experts(w13, torch.ones(2, 2, 1, 1), w2, torch.ones(2, 2, 1))
+    with pytest.raises(ValueError, match="w13_codes"):
+        ops.FP8Experts(w13[:, 0], torch.ones(2, 2, 1, 1), w2, torch.ones(2, 1, 1))
+    with pytest.raises(ValueError, match="CUDA"):
+        ops.FP8Experts(w13, torch.ones(2, 2, 1, 1), w2, torch.ones(2, 1, 1))

@@ -1,0 +1,475 @@
+"""The FP8 operators (E4M3 with a scale per block of 128) on the GPU against their definitions in 64
+bits.
+
+Tolerances.  Quantised codes and scales are exact: scale = rn(amax / 448), code = the E4M3 value nearest
+to the real quotient.  Products: with S = sum |a b| (scaled values), a tensor-core sum of 128 exact
+products is taken to lose at most 2^-22 of S per addition (twice an fp32 half-step), the two scales
+cost 2^-24 each and the additions over the blocks nkb 2^-24, so |error| <= (4 * 128 + nkb + 2) 2^-24 S, plus
+half a step of the output type, finfo(t).eps / 2 of the value.  The layer: see layer_reference."""
+import math
+
+import pytest
+import torch
+
+from nvfp4_mixture_experts_w4a4_b200 import _lib as C
+from nvfp4_mixture_experts_w4a4_b200 import ops
+
+pytestmark = pytest.mark.gpu
+
+BF16_HALF = torch.finfo(torch.bfloat16).eps / 2
+F32_HALF = torch.finfo(torch.float32).eps / 2
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def blocks(n):
+    return -(-n // 128)
+
+
+# ---------------------------------------------------------------------- definitions, 64 bits ----
+def grid():
+    return torch.arange(127, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn).double()
+
+
+def nearest(q):
+    """The E4M3 value nearest to q (fp64), ties to the even code, saturating."""
+    g = grid()
+    a = q.abs()
+    mid = (g[1:] + g[:-1]) / 2
+    lo = torch.searchsorted(mid, a.contiguous(), right=False)
+    hi = torch.searchsorted(mid, a.contiguous(), right=True)   # differs from lo at a tie alone
+    i = torch.where(lo == hi, lo, torch.where(lo % 2 == 0, lo, hi))
+    return torch.copysign(torch.where(a.isnan(), a, g[i]), q)
+
+
+def spread(s, rows, shape):
+    """Scales repeated over their groups."""
+    return s.repeat_interleave(rows, 0)[: shape[0]].repeat_interleave(128, 1)[:, : shape[1]]
+
+
+def quantised(x, rows):
+    """(codes as fp64 values, scales as fp64 holding fp32 values) of a matrix."""
+    R, K = x.shape
+    x = x.double()
+    s = torch.empty(-(-R // rows), blocks(K), dtype=torch.float64, device=x.device)
+    for i in range(s.shape[1]):
+        part = x[:, i * 128:(i + 1) * 128].abs()
+        m = part.amax(1)
+        pad = torch.zeros(s.shape[0] * rows - R, dtype=torch.float64, device=x.device)
+        s[:, i] = torch.cat([m, pad]).view(-1, rows).amax(1)
+    s = (s / 448).float().double()
+    d = spread(s, rows, x.shape)
+    return torch.where(d == 0, torch.zeros_like(x), nearest(x / d)), s
+
+
+def same(a, b):
+    return torch.equal(torch.nan_to_num(a.double(), nan=777.0, posinf=888.0), torch.nan_to_num(b.double(), nan=777.0, posinf=888.0))
+
+
+# ------------------------------------------------------------------------------- quantiser ----
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tile", [ops.FP8_ROWS, ops.FP8_BLOCKS])
+@pytest.mark.parametrize("rows,K", [(1, 1), (1, 128), (3, 127), (129, 129), (130, 1000), (257, 336), (64, 2048),
+                                    (5, 4099)])
+def test_quantize(dtype, tile, rows, K):
+    x = torch.randn(rows, K, generator=gen(rows + K), device="cuda")
+    x[:, ::17] *= 30.0
+    x = x.to(dtype)
+    codes, scale = ops.fp8_quantize(x, tile=tile)
+    q, s = quantised(x, 1 if tile == ops.FP8_ROWS else 128)
+    assert codes.shape == x.shape and codes.dtype == torch.float8_e4m3fn and codes.stride(0) % 16 == 0
+    assert torch.equal(scale.double(), s)
+    assert torch.equal(codes.double(), q)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tile", [ops.FP8_ROWS, ops.FP8_BLOCKS])
+@pytest.mark.parametrize("values", ["borders", "exact scales", "tiny", "subnormal", "huge", "zeros", "not finite"])
+def test_quantize_at_the_edges(dtype, tile, values):
+    g = gen(11)
+    x = torch.randn(200, 700, generator=g, device="cuda")
+    power = torch.exp2(torch.randint(-20, 4, x.shape, generator=g, device="cuda").float())
+    if values == "borders":            # scale 1: every eighth and sixteenth between codes, small ones too
+        x = torch.randint(-255, 256, x.shape, generator=g, device="cuda").float() / 16 * power.clamp(min=2.0 ** -8)
+        x[:, ::128], x[::128] = 448.0, 448.0
+    elif values == "exact scales":     # amax of 7, 14, ... times a power of two divides exactly
+        x = x.bfloat16().float() * power
+        x[:, ::128] = 7.0 * torch.exp2(torch.randint(0, 5, x[:, ::128].shape, generator=g, device="cuda").float())
+    elif values == "tiny":
+        x *= 2.0 ** -110
+    elif values == "subnormal":
+        x *= 2.0 ** -135
+    elif values == "huge":
+        x *= 2.0 ** 120
+    elif values == "zeros":
+        x[:130] = 0.0
+        x[130:, :256] = -0.0
+    else:
+        x[3, 5], x[7, 300], x[140, 699] = math.nan, math.inf, -math.inf
+    x = x.to(dtype)
+    codes, scale = ops.fp8_quantize(x, tile=tile)
+    q, s = quantised(x, 1 if tile == ops.FP8_ROWS else 128)
+    assert same(scale, s)
+    assert same(codes.float(), q)
+
+
+def test_quantize_layouts():
+    """Batches, pitches, slices and outputs of the caller's own; bytes outside them stay."""
+    g = gen(5)
+    wide = torch.randn(3, 40, 300, generator=g, device="cuda")
+    for x in (wide[:, ::2, 3:260], wide[:, :, :256].bfloat16()[:, 5:], wide[1:2, :1, :200]):
+        for tile, rows in ((ops.FP8_ROWS, 1), (ops.FP8_BLOCKS, 128)):
+            B, R, K = x.shape
+            store = torch.full((B, R + 1, K + 7), 99, dtype=torch.uint8, device="cuda")
+            sstore = torch.full((B, -(-R // rows) + 1, blocks(K) + 1), -1.0, device="cuda")
+            codes, scale = store[:, :R, :K], sstore[:, :-1, :-1]
+            c, s = ops.fp8_quantize(x, tile=tile, codes=codes, scale=scale)
+            assert c is codes and s is scale
+            for b in range(B):
+                q, t = quantised(x[b], rows)
+                assert torch.equal(codes[b].clone().view(torch.float8_e4m3fn).double(), q)
+                assert torch.equal(scale[b].double(), t)
+            assert (store[:, R:] == 99).all() and (store[:, :, K:] == 99).all()
+            assert (sstore[:, -1] == -1).all() and (sstore[:, :, -1] == -1).all()
+    c, s = ops.fp8_quantize(torch.empty(0, 64, device="cuda"))
+    assert c.shape == (0, 64) and s.shape == (0, 1)
+
+
+def test_quantize_past_32_bits():
+    """More than 2^32 elements: the last rows are the last rows."""
+    rows, K = 66000, 65552
+    x = torch.zeros(rows, K, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn(3, K, generator=gen(2), device="cuda").bfloat16()
+    codes, scale = ops.fp8_quantize(x)
+    q, s = quantised(x[-3:], 1)
+    assert torch.equal(codes[-3:].double(), q) and torch.equal(scale[-3:].double(), s)
+    assert not codes[-4].view(torch.uint8).any()
+
+
+# --------------------------------------------------------------------------------- product ----
+def matrices(M, N, K, seed, pitch=0):
+    g = gen(seed)
+    a = torch.randn(M, K, generator=g, device="cuda").bfloat16()
+    a[:, ::13] *= 20.0
+    b = torch.randn(N, K, generator=g, device="cuda") / math.sqrt(K)
+    out = []
+    for x, tile in ((a, ops.FP8_ROWS), (b, ops.FP8_BLOCKS)):
+        store = torch.full((x.shape[0], -(-K // 16) * 16 + pitch), 0x7F, dtype=torch.uint8, device="cuda")
+        codes = store.view(torch.float8_e4m3fn)[:, :K]
+        out += ops.fp8_quantize(x, tile=tile, codes=codes)
+    return out
+
+
+def check_gemm(d, a, sa, b, sb):
+    K = a.shape[1]
+    A, B = a.double() * spread(sa.double(), 1, a.shape), b.double() * spread(sb.double(), 128, b.shape)
+    ref, size = A @ B.T, A.abs() @ B.abs().T
+    half = BF16_HALF if d.dtype == torch.bfloat16 else F32_HALF
+    bound = (4 * 128 + blocks(K) + 2) * 2.0 ** -24 * size * (1 + half) + half * ref.abs()
+    assert ((d.double() - ref).abs() <= bound).all(), ((d.double() - ref).abs() / bound).max()
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [
+    (1, 1, 1), (1, 129, 16), (2, 7, 130), (16, 256, 2048), (33, 300, 1003), (77, 2070, 520), (128, 128, 128),
+    (129, 257, 272), (200, 1000, 4096), (256, 512, 640), (300, 700, 2000), (513, 1025, 300), (1000, 2048, 512),
+    (2500, 640, 144), (5, 4000, 8192),
+])
+def test_gemm(M, N, K, out_dtype):
+    """Every way the product is split: single tiles, 128 and 256 columns, K over clusters, pairs of
+    CTAs, sizes that end inside each."""
+    a, sa, b, sb = matrices(M, N, K, M + N)
+    d = ops.fp8_gemm(a, sa, b, sb, out_dtype=out_dtype)
+    check_gemm(d, a, sa, b, sb)
+    assert torch.equal(d, ops.fp8_gemm(a, sa, b, sb, out_dtype=out_dtype))
+    assert ops.device_status() == 0
+
+
+def test_gemm_pitches_and_outputs():
+    """Rows further apart than their length (NaN bytes between them), views of wider scales, an output
+    inside a larger matrix whose surroundings stay, odd pitches and offsets."""
+    for M, N, K in ((150, 333, 392), (40, 96, 1000), (700, 520, 256)):
+        a, sa, b, sb = matrices(M, N, K, 3, pitch=32)
+        wa = torch.full((M, blocks(K) + 3), math.nan, device="cuda")
+        wa[:, 1:1 + blocks(K)] = sa
+        wb = torch.full((blocks(N), blocks(K) + 2), math.nan, device="cuda")
+        wb[:, :blocks(K)] = sb
+        for dtype in (torch.bfloat16, torch.float32):
+            for left in (0, 1, 16):
+                store = torch.full((M + 2, N + 19), -7.0, dtype=dtype, device="cuda")
+                out = store[1:-1, left:left + N]
+                d = ops.fp8_gemm(a, wa[:, 1:1 + blocks(K)], b, wb[:, :blocks(K)], out=out)
+                assert d is out
+                check_gemm(d, a, sa, b, sb)
+                keep = torch.ones_like(store, dtype=torch.bool)
+                keep[1:-1, left:left + N] = False
+                assert (store[keep] == -7).all()
+    a, sa, b, sb = matrices(4, 8, 64, 1)
+    assert ops.fp8_gemm(a[:0], sa[:0], b, sb).shape == (0, 8)
+    assert torch.equal(ops.fp8_gemm(a.view(torch.uint8), sa, b.view(torch.uint8), sb), ops.fp8_gemm(a, sa, b, sb))
+
+
+def test_gemm_keeps_rows_and_blocks_apart():
+    """A NaN or infinite scale, or a NaN code, of one row stays in that row; of one block of B in its
+    columns; a zero scale gives zeros."""
+    a, sa, b, sb = matrices(300, 520, 384, 9)
+    clean = ops.fp8_gemm(a, sa, b, sb, out_dtype=torch.float32)
+    sa, sb, a = sa.clone(), sb.clone(), a.clone()
+    sa[7, 1], sa[150] = math.nan, 0.0
+    a.view(torch.uint8)[290, 5] = 0x7F
+    sb[2, 0] = math.inf                     # columns 256..383
+    d = ops.fp8_gemm(a, sa, b, sb, out_dtype=torch.float32)
+    rows = torch.tensor([r for r in range(300) if r not in (7, 150, 290)], device="cuda")
+    cols = torch.tensor([c for c in range(520) if not 256 <= c < 384], device="cuda")
+    assert torch.equal(d[rows][:, cols], clean[rows][:, cols])
+    assert d[7].isnan().all() and d[290].isnan().all()
+    assert (d[150][cols] == 0).all()
+    assert not d[rows][:, 256:384].isfinite().any()
+
+
+def test_gemm_output_past_32_bits():
+    M, N, K = 70000, 33000, 32
+    a, sa, b, sb = matrices(M, N, K, 4)
+    d = ops.fp8_gemm(a, sa, b, sb)
+    for r in (0, 35000, M - 130):
+        check_gemm(d[r:r + 130], a[r:r + 130], sa[r:r + 130], b, sb)
+
+
+def test_gemm_needs_aligned_rows():
+    a, sa, b, sb = matrices(4, 8, 64, 1)
+    odd = torch.zeros(4, 72, dtype=torch.float8_e4m3fn, device="cuda")[:, :64]
+    with pytest.raises(C.Nvfp4MoeError, match="16 bytes"):
+        ops.fp8_gemm(odd, sa, b, sb)
+    with pytest.raises(ValueError, match="unit stride"):
+        ops.fp8_gemm(torch.zeros(64, 4, dtype=torch.float8_e4m3fn, device="cuda").T, sa, b, sb)
+
+
+# ----------------------------------------------------------------------------------- layer ----
+def experts(E, I, H, seed):
+    g = gen(seed)
+    w = [torch.randn(E, I, H, generator=g, device="cuda") / math.sqrt(H) for _ in range(2)]
+    return ops.FP8Experts.from_float(*w, torch.randn(E, H, I, generator=g, device="cuda") / math.sqrt(I))
+
+
+def layer_reference(w, x, logits, k):
+    """(out, bound) in 64 bits.  The kernels' gate and up sums differ from the real ones by at most
+    eg = (4 * 128 + nkb + 2) 2^-24 of the sums of magnitudes; silu (slope at most 1.1) and its fast
+    exponential and division add 2^-18 of h, so h is off by at most
+      eh = 1.1 eg(g) |u| + |silu(g)| eg(u) + 2^-18 |h|
+    (products of errors are below that).  Its group's scale moves by at most max(eh) / 448 + 2^-24 of it.
+    A code of h can then differ where the real quotient is nearer to a border than the quotient's own
+    error; it differs by the grid's step there (at most |code| / 8, or 2^-9), or a scale that rounds
+    elsewhere moves the dequantised value by its relative change.  The output is off by those, weighted
+    by the down weights and the routing, by the product's own bound, by the softmax's 2^-21 and by half
+    a step of bf16."""
+    T, E = logits.shape
+    H, I = w.H, w.I
+    lg = logits.double()
+    order = torch.sort(lg + 0.0, dim=1, descending=True, stable=True)
+    ids, p = order.indices[:, :k], torch.softmax(order.values[:, :k], 1)
+    xq, xs = quantised(x, 1)
+    xd = xq * spread(xs, 1, x.shape)
+    out = torch.zeros(T, H, dtype=torch.float64, device=x.device)
+    bound = torch.zeros_like(out)
+    es = lambda n: (4 * 128 + blocks(n) + 2) * 2.0 ** -24  # noqa: E731
+    codes = lambda t: t.view(torch.float8_e4m3fn).double()  # noqa: E731
+    mid = (grid()[1:] + grid()[:-1]) / 2
+    for e in ids.unique().tolist():
+        t, j = (ids == e).nonzero(as_tuple=True)
+        wg, wu = (codes(w.w13_codes[e, i].view(torch.uint8)) * spread(w.w13_scale[e, i].double(), 128, (I, H)) for i in (0, 1))
+        wd = codes(w.w2_codes[e].view(torch.uint8)) * spread(w.w2_scale[e].double(), 128, (H, I))
+        xe = xd[t]
+        g, u = xe @ wg.T, xe @ wu.T
+        s = g * torch.sigmoid(g)
+        h = s * u
+        eh = 1.1 * es(H) * (xe.abs() @ wg.abs().T) * u.abs() + s.abs() * es(H) * (xe.abs() @ wu.abs().T) + 2.0 ** -18 * h.abs()
+        hq, hs = quantised(h, 1)
+        S = spread(hs, 1, h.shape)
+        pad = torch.nn.functional.pad(eh, (0, blocks(I) * 128 - I)).view(len(t), -1, 128).amax(2)
+        rel = torch.where(hs > 0, pad / (448 * hs).clamp(min=1e-300), torch.zeros_like(pad)) + 2.0 ** -23
+        rel = spread(rel, 1, h.shape)                                   # relative change of the scale
+        q = torch.where(S > 0, h.abs() / S.clamp(min=1e-300), torch.zeros_like(h))
+        eq = torch.where(S > 0, eh / S.clamp(min=1e-300), torch.zeros_like(h)) + q * rel
+        near = torch.searchsorted(mid, (q - eq).contiguous()) != torch.searchsorted(mid, (q + eq).contiguous(), right=True)
+        step = (q / 8).clamp(min=2.0 ** -9) * 1.2
+        dh = S * (near * step + hq.abs() * rel)
+        y = (hq * S) @ wd.T
+        size = (hq * S).abs() @ wd.abs().T
+        c = p[t, j][:, None]
+        out.index_add_(0, t, c * y)
+        bound.index_add_(0, t, c * (dh @ wd.abs().T + (es(I) + 2.0 ** -21 + k * 2.0 ** -24) * size))
+    return out, bound * (1 + BF16_HALF) + BF16_HALF * out.abs()
+
+
+def check_layer(w, x, logits, k, y):
+    ref, bound = layer_reference(w, x, logits, k)
+    err = (y.double() - ref).abs()
+    assert (err <= bound).all(), (err / bound.clamp(min=1e-300)).max()
+
+
+CASES = [
+    # T, H, I, E, k
+    (1, 256, 128, 8, 2), (1, 2048, 512, 64, 10), (1, 1024, 4096, 1, 1), (2, 16, 16, 3, 3), (3, 144, 80, 5, 1),
+    (8, 256, 128, 8, 2), (15, 1040, 336, 20, 3), (16, 512, 256, 512, 10), (16, 400, 144, 1024, 32), (17, 768, 384, 12, 4),
+    (32, 2048, 128, 40, 8), (32, 256, 128, 1, 1), (33, 256, 128, 8, 2), (45, 1040, 336, 20, 3), (130, 640, 208, 7, 2),
+    (300, 384, 512, 3, 1), (600, 272, 128, 300, 5), (16, 7168, 128, 6, 2), (5, 6144, 256, 4, 2),
+]
+
+
+@pytest.mark.parametrize("T,H,I,E,k", CASES)
+def test_layer(T, H, I, E, k):
+    w = experts(E, I, H, T + E)
+    g = gen(T)
+    x = torch.randn(T, H, generator=g, device="cuda")
+    x[:, ::29] *= 15.0
+    x, logits = x.bfloat16(), torch.randn(T, E, generator=g, device="cuda")
+    layer = ops.FP8MoeFFN(w, k)
+    y = layer(x, logits)
+    check_layer(w, x, logits, k, y)
+    assert torch.equal(y, layer(x, logits))
+    assert ops.device_status() == 0
+
+
+@pytest.mark.parametrize("T", [1, 16, 32])
+@pytest.mark.parametrize("launch", [C.LAUNCH_SINGLE, C.LAUNCH_MULTI])
+def test_layer_launches(T, launch):
+    """Both ways of running a small batch, workspaces reused across changing routings."""
+    w = experts(24, 272, 528, 1)
+    layer = ops.FP8MoeFFN(w, 4, launch=launch)
+    for seed in range(4):
+        g = gen(seed)
+        x = torch.randn(T, 528, generator=g, device="cuda").bfloat16()
+        logits = torch.randn(T, 24, generator=g, device="cuda")
+        if seed == 1:      # one expert gets every token
+            logits[:, 5] += 100.0
+        if seed == 2:      # equal logits: the lowest experts
+            logits[:] = 0.25
+        if seed == 3:      # one token alone among the others' experts
+            logits[0] = -logits[0]
+        check_layer(w, x, logits, 4, layer(x, logits))
+    assert ops.device_status() == 0
+
+
+@pytest.mark.parametrize("T", [12, 100])
+def test_layer_rows_stay_apart(T):
+    """A token of NaN, one of infinities and one of zeros leave the other tokens' bits alone."""
+    w = experts(6, 128, 256, 2)
+    g = gen(3)
+    x, logits = torch.randn(T, 256, generator=g, device="cuda").bfloat16(), torch.randn(T, 6, generator=g, device="cuda")
+    layer = ops.FP8MoeFFN(w, 2)
+    clean = layer(x, logits)
+    x[2], x[5, 100], x[7] = math.nan, math.inf, 0.0
+    y = layer(x, logits)
+    others = torch.tensor([t for t in range(T) if t not in (2, 5, 7)], device="cuda")
+    assert torch.equal(y[others], clean[others])
+    assert y[2].isnan().all() and not y[5].isfinite().any() and (y[7] == 0).all()
+
+
+def test_layer_inputs_and_outputs():
+    """Strided x and logits, other logit types, an output of the caller's own, an empty batch."""
+    w = experts(8, 128, 256, 4)
+    layer = ops.FP8MoeFFN(w, 2)
+    g = gen(6)
+    x, logits = torch.randn(40, 512, generator=g, device="cuda").bfloat16(), torch.randn(40, 16, generator=g, device="cuda")
+    y = layer(x[::2, :256], logits[::2, ::2])
+    assert torch.equal(y, layer(x[::2, :256].contiguous(), logits[::2, ::2].contiguous()))
+    half = logits[::2, ::2].bfloat16()
+    assert torch.equal(layer(x[::2, :256], half), layer(x[::2, :256], half.float()))
+    out = torch.empty(20, 256, dtype=torch.bfloat16, device="cuda")
+    assert layer(x[::2, :256], logits[::2, ::2], out=out) is out and torch.equal(out, y)
+    assert layer(x[:0, :256], logits[:0, :8]).shape == (0, 256)
+    for bad in (dict(x=x[:4].float()[:, :256], logits=logits[:4, :8]), dict(x=x[:4], logits=logits[:4, :8]),
+                dict(x=x[:4, :256], logits=logits[:5, :8]), dict(x=x[:4, :256], logits=logits[:4, :8], out=out)):
+        with pytest.raises(ValueError):
+            layer(**bad)
+    with pytest.raises(C.Nvfp4MoeError, match="single launch"):
+        ops.FP8MoeFFN(w, 2, launch=C.LAUNCH_SINGLE)(x[:33, :256], logits[:33, :8])
+    with pytest.raises(C.Nvfp4MoeError, match="multiple of 16"):
+        ops.FP8MoeFFN(experts(2, 24, 256, 1), 1)(x[:4, :256], logits[:4, :2])
+
+
+def test_experts_from_codes():
+    """from_fp8 keeps codes and scales as they are; from_float is fp8_quantize's blocks."""
+    g = gen(8)
+    ws = [torch.randn(3, n, k, generator=g, device="cuda") for n, k in ((144, 272), (144, 272), (272, 144))]
+    q = [ops.fp8_quantize(v, tile=ops.FP8_BLOCKS) for v in ws]
+    a, b = ops.FP8Experts.from_fp8(*q), ops.FP8Experts.from_float(*ws)
+    for n in ("w13_codes", "w2_codes"):
+        assert torch.equal(getattr(a, n).view(torch.uint8), getattr(b, n).view(torch.uint8))
+    assert torch.equal(a.w13_scale, b.w13_scale) and torch.equal(a.w2_scale, b.w2_scale)
+    for i, (c, s) in enumerate(q):
+        for e in range(3):
+            r, t = quantised(ws[i][e], 128)
+            assert torch.equal(c[e].double(), r) and torch.equal(s[e].double(), t)
+
+
+# ---------------------------------------------------------------------- streams, graphs, together ----
+@pytest.mark.parametrize("T", [4, 60])
+def test_graphs_share_a_workspace(T):
+    """Two captured calls on one layer's workspace, replayed in turn with an eager call between, and on
+    a stream of their own."""
+    w = experts(16, 256, 512, 5)
+    layer = ops.FP8MoeFFN(w, 3)
+    g = gen(T)
+    xs = [torch.randn(T, 512, generator=g, device="cuda").bfloat16() for _ in range(4)]
+    ls = [torch.randn(T, 16, generator=g, device="cuda") for _ in range(4)]
+    want = [layer(x, l) for x, l in zip(xs, ls)]
+    a, b = ops.GraphedMoeFFN(layer, T), ops.GraphedMoeFFN(layer, T)
+    for i in range(4):
+        assert torch.equal(a(xs[i], ls[i]), want[i])
+        assert torch.equal(layer(xs[i ^ 1], ls[i ^ 1]), want[i ^ 1])
+        assert torch.equal(b(xs[3 - i], ls[3 - i]), want[3 - i])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = [layer(x, l) for x, l in zip(xs, ls)]
+    side.synchronize()
+    assert all(torch.equal(y, z) for y, z in zip(got, want))
+    io = ops.GraphedMoeFFN(layer, T, host_io=True)
+    y = io(xs[0].cpu(), ls[0].cpu())
+    torch.cuda.synchronize()
+    assert torch.equal(y.cuda(), want[0])
+
+
+def test_quantize_and_gemm_on_streams_and_in_graphs():
+    g = gen(1)
+    x, wt = torch.randn(70, 640, generator=g, device="cuda").bfloat16(), torch.randn(900, 640, generator=g, device="cuda")
+    b, sb = ops.fp8_quantize(wt, tile=ops.FP8_BLOCKS)
+    want = ops.fp8_gemm(*ops.fp8_quantize(x), b, sb)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = ops.fp8_gemm(*ops.fp8_quantize(x), b, sb)
+    side.synchronize()
+    assert torch.equal(got, want)
+    graph, static = torch.cuda.CUDAGraph(), torch.zeros_like(x)
+    with torch.cuda.graph(graph):
+        out = ops.fp8_gemm(*ops.fp8_quantize(static), b, sb)
+    static.copy_(x)
+    graph.replay()
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("T", [1, 24, 200])
+def test_a_block_of_a_model(T):
+    """The operators as a model's block uses them: a projection, the router on its output, the routed
+    layer, a projection back; each against its definition on the inputs that it got."""
+    g = gen(T)
+    H, E, k = 512, 12, 3
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    proj, sp = ops.fp8_quantize(torch.randn(H, H, generator=g, device="cuda") / math.sqrt(H), tile=ops.FP8_BLOCKS)
+    router, sr = ops.fp8_quantize(torch.randn(E, H, generator=g, device="cuda") / math.sqrt(H), tile=ops.FP8_BLOCKS)
+    w = experts(E, 256, H, 3)
+    a, sa = ops.fp8_quantize(x)
+    y = ops.fp8_gemm(a, sa, proj, sp)
+    check_gemm(y, a, sa, proj, sp)
+    b, sb = ops.fp8_quantize(y)
+    logits = ops.fp8_gemm(b, sb, router, sr, out_dtype=torch.float32)
+    check_gemm(logits, b, sb, router, sr)
+    z = ops.FP8MoeFFN(w, k)(y, logits)
+    check_layer(w, y, logits, k, z)
+    c, sc = ops.fp8_quantize(z)
+    check_gemm(ops.fp8_gemm(c, sc, proj, sp), c, sc, proj, sp)
+    assert ops.device_status() == 0
