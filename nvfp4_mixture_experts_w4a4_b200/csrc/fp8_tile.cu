@@ -732,9 +732,9 @@ int resident_clusters(int split) {
 
 // How a dense product is run: the width of a tile, the CTAs that split its K, and whether pairs of
 // CTAs take 256 rows.  The estimate, in microseconds fitted to measurements on a B200: every round of
-// resident tiles costs its blocks of K (a 128 x 128 tile's in 0.30, a 128 x 256 tile's in 0.62, a
-// pair's in 0.58) and 1.0 for its start and end; a split tile 1.5 + 0.6 a CTA instead, for the
-// exchange.  E.g. 64 x 4096 x 4096: 11.5 measured with 128 columns split over 4, 16.1 unsplit, 27.7
+// resident tiles costs its blocks of K (a 128 x 128 tile's in 0.30, or 0.36 where more than half of the
+// SMs are busy, a 128 x 256 tile's in 0.62, a pair's in 0.58) and 1.0 for its start and end; a split
+// tile 2.0 + 0.8 a CTA instead, for the exchange.  E.g. 64 x 4096 x 4096: 11.5 measured with 128 columns split over 4, 16.1 unsplit, 27.7
 // over 8 (clusters of 8 do not all fit at once); 2048 x 4096 x 4096: 42.6 in pairs, 46.3 unpaired.
 DensePlan fp8_dense_plan(int64_t M, int64_t N, int64_t K) {
   const int sms = num_sms();
@@ -748,8 +748,9 @@ DensePlan fp8_dense_plan(int64_t M, int64_t N, int64_t K) {
     for (int split = 1; split <= kMaxSplit; ++split) {
       if (split > 1 && (split > nkb || tiles * split > sms)) break;
       const int64_t at_once = split == 1 ? sms : (bn == 256 ? resident_clusters<256>(split) : resident_clusters<128>(split));
-      const double cost = rounds(tiles, at_once) * (((nkb + split - 1) / split) * (bn == 256 ? 0.62 : 0.30) +
-                                                    (split > 1 ? 1.5 + 0.6 * split : 1.0));
+      const double block = bn == 256 ? 0.62 : (tiles * split > sms / 2 ? 0.36 : 0.30);
+      const double cost =
+          rounds(tiles, at_once) * (((nkb + split - 1) / split) * block + (split > 1 ? 2.0 + 0.8 * split : 1.0));
       if (cost < least) {
         least = cost;
         best = DensePlan{bn, split, false};
