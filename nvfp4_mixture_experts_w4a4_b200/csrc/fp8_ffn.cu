@@ -9,15 +9,16 @@ namespace nvfp4moe {
 namespace {
 
 constexpr int kPlaceThreads = 256;
-constexpr int kRowTile = 128;
+constexpr int kRowTile = 128;  // rows of a tile of the grouped products
 
 // x [T][H] bf16 -> E4M3 rows in expert order: each 128-element group is quantised once (half a
 // warp, 16 bytes a lane) and written to the k rows of its token.  Block 0 writes the list of row
-// tiles instead: {expert, first row, rows} for every 128 rows of every expert, [0].x their number.
+// groups instead ({expert, first row, rows} for every `group` rows of every expert, [0].x their number) and
+// zeroes a counter for each.
 __global__ void __launch_bounds__(kPlaceThreads)
 fp8_place_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ pair_to_row,
                  const int32_t* __restrict__ offsets, int T, int H, int E, int k, uint8_t* __restrict__ codes,
-                 float* __restrict__ scale, int4* __restrict__ tiles) {
+                 float* __restrict__ scale, int group, int4* __restrict__ tiles, int* __restrict__ counters) {
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -31,7 +32,7 @@ fp8_place_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict_
       const int e = e0 + i;
       first[i] = e < E ? offsets[e] : 0;
       n[i] = e < E ? offsets[e + 1] - first[i] : 0;
-      mine += (n[i] + kRowTile - 1) / kRowTile;
+      mine += (n[i] + group - 1) / group;
     }
     int incl = mine;
 #pragma unroll
@@ -48,7 +49,8 @@ fp8_place_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict_
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      for (int r = 0; r < n[i]; r += kRowTile) tiles[1 + at++] = make_int4(e0 + i, first[i] + r, min(kRowTile, n[i] - r), 0);
+      for (int r = 0; r < n[i]; r += group) tiles[1 + at++] = make_int4(e0 + i, first[i] + r, min(group, n[i] - r), 0);
+    for (int i = threadIdx.x; i < total; i += kPlaceThreads) counters[i] = 0;
     if (threadIdx.x == 0) tiles[0] = make_int4(total, 0, 0, 0);
     return;
   }
@@ -88,7 +90,7 @@ struct Layout {
   int64_t ids, w, counts, offsets, padded, pair_to_row, row_token, row_pair, tile_expert, active, scratch, tiles,
       x_codes, x_scale, h_codes, h_scale, slots, counters, parts, total;
   int64_t pairs;
-  int max_row_tiles;
+  int group, max_row_tiles;  // rows of a group, groups at most
   bool single;
 };
 
@@ -126,7 +128,8 @@ Layout make_layout(const fp8_moe_ffn_desc& d) {
   };
   const int64_t P = int64_t(d.T) * d.top_k, nH = fp8_blocks(d.H), nI = fp8_blocks(d.I);
   L.pairs = P;
-  L.max_row_tiles = int(P / kRowTile + (P < d.E ? P : d.E));
+  L.group = fp8_stream_rows(P, d.E) > 0 ? fp8_stream_rows(P, d.E) : kRowTile;
+  L.max_row_tiles = int(P / L.group + (P < d.E ? P : d.E));
   L.single = takes_single(d);
   if (L.single) {
     const Fp8LayerSizes z = fp8_layer_sizes(d.T, d.H, d.I, d.E, d.top_k);
@@ -142,6 +145,7 @@ Layout make_layout(const fp8_moe_ffn_desc& d) {
   L.active = put((d.E + 1) * 4);
   L.scratch = put(d.T > 0 ? batch_prologue_scratch_bytes(d.T, d.E) : 0);
   L.tiles = put((int64_t(L.max_row_tiles) + 1) * 16);
+  L.counters = put(int64_t(L.max_row_tiles) * 4);
   L.x_codes = put(P * d.H), L.x_scale = put(P * nH * 4);
   L.h_codes = put(P * d.I), L.h_scale = put(P * nI * 4);
   L.slots = put(P * d.H * 4);
@@ -201,7 +205,8 @@ nvfp4moe_status fp8_moe_ffn_forward(const fp8_moe_ffn_desc* desc, const void* x,
                                          dim3(kPlaceThreads), 0, s, static_cast<const __nv_bfloat16*>(x),
                                          static_cast<const int32_t*>(i32(L.pair_to_row)),
                                          static_cast<const int32_t*>(i32(L.offsets)), int(d.T), int(d.H), int(d.E),
-                                         int(d.top_k), ws + L.x_codes, f32(L.x_scale), tiles);
+                                         int(d.top_k), ws + L.x_codes, f32(L.x_scale), L.group, tiles,
+                                         i32(L.counters));
   NVFP4_REQUIRE(e == cudaSuccess, NVFP4MOE_CUDA_ERROR, "%s: %s", fn, cudaGetErrorString(e));
   GroupedArgs g{};
   g.H = d.H, g.I = d.I, g.E = d.E;
@@ -211,7 +216,7 @@ nvfp4moe_status fp8_moe_ffn_forward(const fp8_moe_ffn_desc* desc, const void* x,
   g.x_codes = ws + L.x_codes, g.x_scale = f32(L.x_scale);
   g.w13_codes = d.w13_codes, g.w13_scale = d.w13_scale, g.w2_codes = d.w2_codes, g.w2_scale = d.w2_scale;
   g.h_codes = ws + L.h_codes, g.h_scale = f32(L.h_scale), g.slots = f32(L.slots);
-  st = launch_fp8_grouped(g, s);
+  st = L.group == kRowTile ? launch_fp8_grouped(g, s) : launch_fp8_stream(g, L.group, i32(L.counters), s);
   if (st != NVFP4MOE_OK) return st;
   return launch_combine_rows(f32(L.slots), i32(L.pair_to_row), f32(L.w), d.T, d.H, d.top_k, out, s);
 }

@@ -21,6 +21,10 @@
 // Combine: after a grid-wide barrier every CTA sums a slice of the outputs over the k slots of a
 // token, in slot order, and rounds once.
 //
+// GROUPED is the same stream for larger batches whose experts get few rows each: the routing and x in
+// expert order come from launches before, units take at most NT rows of an expert, x comes per stage
+// as h does, and the rows of the output stay in expert order for the combine's own launch.
+//
 // Warps: 0 streams weights (TMA); 1 owns TMEM and issues the MMAs; 2 and 3 fetch x and its scales;
 // 4..7 add and finish the first tile of every stage, 8..11 the second; 12..15 take every fourth stage
 // each and fetch its scales, and h for down stages (four, because each waits out an L2 read a stage:
@@ -41,7 +45,7 @@ constexpr int kThreads = 512;
 constexpr int kTile = 128 * 128;         // bytes of a weight tile
 constexpr int kStage = 2 * kTile;
 constexpr int kMaxStages = 6, kMinStages = 3;  // (more than 8 or less than 3: see the scale warps)
-constexpr int kSlots = 8;                // accumulator slots (stages in flight past the MMA)
+constexpr int slots_of(int nt) { return nt == 64 ? 4 : 8; }  // accumulator slots (stages past the MMA)
 constexpr int kMaxE = 1024;
 constexpr int kPitch = 132;              // floats of a row of the exchange buffer
 constexpr int kSmemLimit = 226 * 1024;   // dynamic; a few hundred bytes more are static
@@ -53,7 +57,8 @@ __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; 
 
 struct LayerArgs {
   const float* logits;
-  const float* x_scale;    // [T][nH]
+  const float* x_scale;    // [T][nH]; GROUPED: [pairs][nH]
+  const int4* list;        // GROUPED: [0].x row groups, then {expert, first row, rows, -} each
   int T, H, I, E, k;
   int nH, nI;              // 128-blocks
   int stages;
@@ -76,7 +81,8 @@ struct LayerArgs {
 struct Smem {
   int h, x, xs, sb, hs, buf, mask, list, row0, rowof, ids, w, bars, total;
 };
-__host__ __device__ inline Smem smem_layout(int nt, int nH, int k, int E, int stages) {
+__host__ __device__ inline Smem smem_layout(int nt, int nH, int k, int E, int stages, bool grouped) {
+  if (grouped) nH = 0, k = 0, E = 0;  // no x, no routing
   Smem m;
   int at = stages * kStage;
   auto put = [&](int bytes) {
@@ -87,8 +93,8 @@ __host__ __device__ inline Smem smem_layout(int nt, int nH, int k, int E, int st
   m.h = put(stages * 2 * nt * 128);
   m.x = put(nH * nt * 128);
   m.xs = put(nH * nt * 4);
-  m.sb = put(kSlots * 2 * 4);
-  m.hs = put(kSlots * 2 * nt * 4);
+  m.sb = put(slots_of(nt) * 2 * 4);
+  m.hs = put(slots_of(nt) * 2 * nt * 4);
   m.buf = put(nt * kPitch * 4);
   const int most = nt * k < E ? nt * k : E;
   m.mask = put(E * 4);
@@ -97,7 +103,7 @@ __host__ __device__ inline Smem smem_layout(int nt, int nH, int k, int E, int st
   m.row0 = put((most + 1) * 4);
   m.ids = put(nt * k * 4);
   m.w = put(nt * k * 4);
-  m.bars = put((2 * kMaxStages + 2 * kSlots + 4) * 8);
+  m.bars = put((2 * kMaxStages + 2 * slots_of(nt) + 4) * 8);
   m.total = at + 1024;
   return m;
 }
@@ -106,20 +112,20 @@ __host__ __device__ inline Smem smem_layout(int nt, int nH, int k, int E, int st
 // touched (A) and the grid.
 struct Plan {
   int A, G, s1, s2, n1, n2, extra, light, heavy, first2;
-  __device__ Plan(const LayerArgs& a, int active, int grid, int cta) {
+  __device__ Plan(const LayerArgs& a, int active, int grid, int cta, bool grouped) {
     A = active, G = grid;
     s1 = 1, s2 = 1;
     const int u1 = A * a.nI, u2 = A * a.nH, st2 = ceil_div(a.nI, 2);
     // Parts of a unit: the count with the fewest stages in the fullest CTA, a split gate/up unit
     // costing six stages for the exchange of its parts and a down unit one for its end.  A lane tries one count.
     const int s = (threadIdx.x & 31) + 1;
-    if (u1 < G) {
+    if (!grouped && u1 < G) {
       int cost = INT32_MAX;
       if (s <= kMaxSplit && s <= a.nH && u1 * s <= a.max_parts)
         cost = (ceil_div(u1 * s, G) * (ceil_div(a.nH, s) + (s > 1 ? 6 : 0))) * 32 + s - 1;
       s1 = (__reduce_min_sync(0xffffffffu, cost) & 31) + 1;
     }
-    if (u2 < 4 * G) {
+    if (!grouped && u2 < 4 * G) {
       int cost = INT32_MAX;
       if (s <= a.chunks_cap && s <= st2) cost = ceil_div(u2 * s, G) * (ceil_div(st2, s) + 1) * 32 + s - 1;
       s2 = (__reduce_min_sync(0xffffffffu, cost) & 31) + 1;
@@ -219,9 +225,9 @@ __device__ __forceinline__ bool wait_count(const int* p, int want) {
 }
 __device__ __forceinline__ void add_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-template <int NT>
-__device__ __forceinline__ void read_columns(uint32_t taddr, uint32_t (&r)[NT]) {
-  if constexpr (NT == 32) {
+template <int N>
+__device__ __forceinline__ void read_columns(uint32_t taddr, uint32_t (&r)[N]) {
+  if constexpr (N == 32) {
     tmem_ld_32x32b_x32(taddr, r);
   } else {
     asm volatile(
@@ -278,13 +284,14 @@ fp8_layer_prepare_kernel(const __nv_bfloat16* __restrict__ x, int T, int H, uint
   if (sub == 0) scale[t * nH + kb] = f.scale;
 }
 
-template <int NT, int PER_LANE>
+template <int NT, int PER_LANE, bool GROUPED>
 __global__ void __launch_bounds__(kThreads, 1)
 fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant__ CUtensorMap tm2,
                  const __grid_constant__ CUtensorMap tmh, const __grid_constant__ CUtensorMap tmx, const LayerArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_shared_1024(smem_raw);
-  const Smem m = smem_layout(NT, a.nH, a.k, a.E, a.stages);
+  const Smem m = smem_layout(NT, a.nH, a.k, a.E, a.stages, GROUPED);
+  constexpr int kSlots = slots_of(NT);
   float* s_xs = reinterpret_cast<float*>(smem + m.xs);          // [nH][NT]
   float* s_sb = reinterpret_cast<float*>(smem + m.sb);          // [slot][2]
   float* s_hs = reinterpret_cast<float*>(smem + m.hs);          // [slot][2][NT]
@@ -314,8 +321,8 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
   const int W = a.stages >= 4 ? 4 : 3;
 
   // ---- set-up, with the logits on their way ----
-  constexpr int TOK = NT / 16;  // tokens a warp routes
-  float lg[TOK][PER_LANE];
+  constexpr int TOK = GROUPED ? 0 : NT / 16;  // tokens a warp routes
+  float lg[TOK + GROUPED][PER_LANE];
 #pragma unroll
   for (int i = 0; i < TOK; ++i) {
     const int t = warp + 16 * i;
@@ -349,7 +356,8 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
     prefetch_tensormap(&tmh);
     prefetch_tensormap(&tmx);
   }
-  for (int e = threadIdx.x; e < a.E; e += kThreads) s_mask[e] = 0u;
+  if constexpr (!GROUPED)
+    for (int e = threadIdx.x; e < a.E; e += kThreads) s_mask[e] = 0u;
   __syncthreads();
 
   // ---- routing and the list of touched experts ----
@@ -367,8 +375,11 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
       }
     }
   }
-  __syncthreads();
-  {
+  if constexpr (GROUPED) {
+    griddep_wait();  // the list, x and the counters come from the launches before
+    griddep_launch_dependents();
+  } else {
+    __syncthreads();
     static_assert(kMaxE == 2 * kThreads, "two experts a thread");
     int n[2], act = 0, rows = 0;
 #pragma unroll
@@ -409,12 +420,24 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_holder;
-  const Plan p(a, s_active, int(gridDim.x), cta);
+  const Plan p(a, GROUPED ? a.list[0].x : s_active, int(gridDim.x), cta, GROUPED);
   const int units = p.units();
   const int S = a.stages;
   auto abort_now = [&]() {
     abort_flag = 1;
     atomicOr(a.status, kTimeout);
+  };
+  // the expert of a unit, its first row in expert order and its rows
+  struct Rows {
+    int e, row0, n;
+  };
+  auto rows_of = [&](const Unit& u) {
+    if constexpr (GROUPED) {
+      const int4 q = __ldg(a.list + 1 + u.a);
+      return Rows{q.x, q.y, q.z};
+    } else {
+      return Rows{s_list[u.a], s_row0[u.a], s_row0[u.a + 1] - s_row0[u.a]};
+    }
   };
 
   if (warp == 0) {
@@ -422,7 +445,7 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
       uint32_t it = 0;
       for (int i = 0; i < units && !abort_flag; ++i) {
         const Unit u = unit_of(p, a, i, cta);
-        const int e = s_list[u.a];
+        const int e = rows_of(u).e;
         for (int j = u.j0; j < u.j1; ++j, ++it) {
           const int s = it % S;
           if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1)) {
@@ -450,7 +473,7 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
     if (elect_one()) {
       constexpr uint32_t idesc = (1u << 4) | (uint32_t(NT >> 3) << 17) | (uint32_t(128 >> 4) << 24);
       uint32_t it = 0;
-      bool ok = mbar_wait(x_full, 0);
+      bool ok = GROUPED || mbar_wait(x_full, 0);
       if (!ok) abort_now();
       for (int i = 0; i < units && ok && !abort_flag; ++i) {
         const Unit u = unit_of(p, a, i, cta);
@@ -465,7 +488,9 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint64_t ad = desc_kmajor_sw128(smem + s * kStage + h * kTile);
-            const uint64_t bd = desc_kmajor_sw128(u.down ? smem + m.h + (2 * s + h) * NT * 128 : smem + m.x + j * NT * 128);
+            const uint8_t* b = u.down ? smem + m.h + (2 * s + h) * NT * 128
+                                      : (GROUPED ? smem + m.h + 2 * s * NT * 128 : smem + m.x + j * NT * 128);
+            const uint64_t bd = desc_kmajor_sw128(b);
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               mma_f8(tmem + (2 * slot + h) * NT, ad + 2 * q, bd + 2 * q, idesc, q != 0 ? 1u : 0u);
@@ -477,13 +502,13 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
       tc_commit(drain);
       mbar_wait(drain, 0, 1u << 20);
     }
-  } else if (warp == 2) {
+  } else if (warp == 2 && !GROUPED) {
     griddep_wait();  // x comes from the launch before
     if (elect_one()) {
       mbar_arrive_expect_tx(x_full, a.nH * NT * 128);
       for (int kb = 0; kb < a.nH; ++kb) load_tile(smem + m.x + kb * NT * 128, &tmx, kb * 128, 0, 0, x_full);
     }
-  } else if (warp == 3) {
+  } else if (warp == 3 && !GROUPED) {
     griddep_wait();
     for (int i = lane; i < a.nH * a.T; i += 32) {
       const int t = i / a.nH, kb = i - t * a.nH;
@@ -498,7 +523,7 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
     griddep_wait();  // the counters are zero
     for (int i = 0; i < units && ok && !abort_flag; ++i) {
       const Unit u = unit_of(p, a, i, cta);
-      const int e = s_list[u.a], row0 = s_row0[u.a], n = s_row0[u.a + 1] - row0;
+      const auto [e, row0, n] = rows_of(u);
       for (int j = u.j0; j < u.j1; ++j, ++it) {
         if (int(it % W) != warp - 12) continue;
         const int s = it % S, slot = it % kSlots;
@@ -528,16 +553,25 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
             load_tile(smem + m.h + 2 * s * NT * 128, &tmh, 2 * j * 128, row0, 0, &full[s]);
             load_tile(smem + m.h + (2 * s + 1) * NT * 128, &tmh, (2 * j + 1) * 128, row0, 0, &full[s]);
           }
-          float hs[2] = {0.0f, 0.0f};
-          if (lane < n) {
-            const float* q = a.h_scale + int64_t(row0 + lane) * a.nI + 2 * j;
-            hs[0] = __ldcg(q);
-            if (2 * j + 1 < a.nI) hs[1] = __ldcg(q + 1);
+#pragma unroll
+          for (int c = lane; c < NT; c += 32) {
+            float hs[2] = {0.0f, 0.0f};
+            if (c < n) {
+              const float* q = a.h_scale + int64_t(row0 + c) * a.nI + 2 * j;
+              hs[0] = __ldcg(q);
+              if (2 * j + 1 < a.nI) hs[1] = __ldcg(q + 1);
+            }
+            s_hs[(2 * slot) * NT + c] = hs[0];
+            s_hs[(2 * slot + 1) * NT + c] = hs[1];
           }
-          if (lane < NT) {
-            s_hs[(2 * slot) * NT + lane] = hs[0];
-            s_hs[(2 * slot + 1) * NT + lane] = hs[1];
+        } else if constexpr (GROUPED) {
+          if (lane == 0) {
+            mbar_expect_tx(&full[s], NT * 128);
+            load_tile(smem + m.h + 2 * s * NT * 128, &tmx, j * 128, row0, 0, &full[s]);
           }
+#pragma unroll
+          for (int c = lane; c < NT; c += 32)
+            s_hs[(2 * slot) * NT + c] = c < n ? __ldg(a.x_scale + int64_t(row0 + c) * a.nH + j) : 0.0f;
         }
         if (lane < 2) s_sb[2 * slot + lane] = sb;
         __syncwarp();
@@ -547,13 +581,13 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
   } else if (warp >= 4 && warp < 12) {
     const int half = (warp - 4) >> 2, q = warp & 3, r = q * 32 + lane;
     const uint32_t trow = tmem + (uint32_t(q * 32) << 16);
-    bool ok = mbar_wait(x_full, 0);
+    bool ok = GROUPED || mbar_wait(x_full, 0);
     if (!ok) abort_now();
     griddep_wait();  // the counters are zero
     uint32_t it = 0;
     for (int i = 0; i < units && ok; ++i) {
       const Unit u = unit_of(p, a, i, cta);
-      const int e = s_list[u.a], row0 = s_row0[u.a], n = s_row0[u.a + 1] - row0;
+      const auto [e, row0, n] = rows_of(u);
       float acc[NT];
 #pragma unroll
       for (int c = 0; c < NT; ++c) acc[c] = 0.0f;
@@ -565,17 +599,23 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
           break;
         }
         tc_fence_after();
-        uint32_t v[NT];
-        read_columns<NT>(trow + (2 * slot + half) * NT, v);
         const float sb = s_sb[2 * slot + half];
-        const float4* sc = reinterpret_cast<const float4*>(u.down ? s_hs + (2 * slot + half) * NT : s_xs + j * NT);
+        const float4* sc = reinterpret_cast<const float4*>(
+            u.down ? s_hs + (2 * slot + half) * NT : (GROUPED ? s_hs + 2 * slot * NT : s_xs + j * NT));
+        constexpr int CW = NT < 32 ? NT : 32;
 #pragma unroll
-        for (int c = 0; c < NT; c += 4) {
-          const float4 f = sc[c / 4];
-          acc[c] = fmaf(__uint_as_float(v[c]), f.x * sb, acc[c]);
-          acc[c + 1] = fmaf(__uint_as_float(v[c + 1]), f.y * sb, acc[c + 1]);
-          acc[c + 2] = fmaf(__uint_as_float(v[c + 2]), f.z * sb, acc[c + 2]);
-          acc[c + 3] = fmaf(__uint_as_float(v[c + 3]), f.w * sb, acc[c + 3]);
+        for (int c0 = 0; c0 < NT; c0 += CW) {
+          if (GROUPED && c0 >= n) break;  // columns without rows
+          uint32_t v[CW];
+          read_columns<CW>(trow + (2 * slot + half) * NT + c0, v);
+#pragma unroll
+          for (int c = 0; c < CW; c += 4) {
+            const float4 f = sc[(c0 + c) / 4];
+            acc[c0 + c] = fmaf(__uint_as_float(v[c]), f.x * sb, acc[c0 + c]);
+            acc[c0 + c + 1] = fmaf(__uint_as_float(v[c + 1]), f.y * sb, acc[c0 + c + 1]);
+            acc[c0 + c + 2] = fmaf(__uint_as_float(v[c + 2]), f.z * sb, acc[c0 + c + 2]);
+            acc[c0 + c + 3] = fmaf(__uint_as_float(v[c + 3]), f.w * sb, acc[c0 + c + 3]);
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -600,7 +640,7 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
         add_barrier();
       } else {
         bool finish = true;
-        if (p.s1 > 1) {
+        if (!GROUPED && p.s1 > 1) {
           // this part's sums; the last part to arrive adds all of them in order
           float* dst = a.parts + ((int64_t(u.id) * p.s1 + u.part) * 2 + half) * NT * 128 + r;
 #pragma unroll
@@ -634,10 +674,10 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
           }
           add_barrier();
           // a warp takes every eighth token of the expert: 128 columns, one group
-          const uint32_t mask = s_mask[e];
+          const uint32_t mask = GROUPED ? 0u : s_mask[e];
           const int i0 = u.blk * 128 + lane * 4;
           for (int c = warp - 4; c < n; c += 8) {
-            const int t = __fns(mask, 0, c + 1);  // the token's column
+            const int t = GROUPED ? c : int(__fns(mask, 0, c + 1));  // the token's column
             const float4 h = *reinterpret_cast<const float4*>(s_buf + t * kPitch + lane * 4);
             const uint32_t mx = __reduce_max_sync(
                 0xffffffffu, max(max(abs_bits(h.x), abs_bits(h.y)), max(abs_bits(h.z), abs_bits(h.w))));
@@ -653,13 +693,13 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
       }
     }
     // ---- combine ----
-    add_barrier();
-    if (threadIdx.x == 128) {
+    if constexpr (!GROUPED) add_barrier();
+    if (!GROUPED && threadIdx.x == 128) {
       add_release(a.gbar);
       if (!wait_count(a.gbar, int(gridDim.x))) abort_now();
     }
-    add_barrier();
-    if (!abort_flag) {
+    if constexpr (!GROUPED) add_barrier();
+    if (!GROUPED && !abort_flag) {
       const int per_row = a.H / 4;
       const int total = a.T * per_row, stride = int(gridDim.x) * 256;
       for (int i = cta * 256 + int(threadIdx.x) - 128; i < total; i += stride) {
@@ -694,7 +734,7 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
 int columns_for(int T) { return T <= 16 ? 16 : 32; }
 int stages_for(int T, int H, int E, int k) {
   for (int s = kMaxStages; s >= kMinStages; --s)
-    if (smem_layout(columns_for(T), int(fp8_blocks(H)), k, E, s).total <= kSmemLimit) return s;
+    if (smem_layout(columns_for(T), int(fp8_blocks(H)), k, E, s, false).total <= kSmemLimit) return s;
   return 0;
 }
 // K chunks of a down unit at most: enough for the fewest units there can be (one expert)
@@ -705,10 +745,10 @@ int chunks_for(int H, int I) {
 }
 constexpr int kMaxParts = 4 * 148;
 
-template <int NT, int PER_LANE>
+template <int NT, int PER_LANE, bool GROUPED = false>
 cudaError_t launch_one(const CUtensorMap& m13, const CUtensorMap& m2, const CUtensorMap& mh, const CUtensorMap& mx, const LayerArgs& a,
                        int grid, size_t smem, cudaStream_t s) {
-  constexpr auto kern = fp8_layer_kernel<NT, PER_LANE>;
+  constexpr auto kern = fp8_layer_kernel<NT, PER_LANE, GROUPED>;
   const cudaError_t e = set_smem_limit_once<kern>(kSmemLimit);
   return e != cudaSuccess ? e : launch_cooperative_dependent(kern, dim3(grid), dim3(kThreads), smem, s, m13, m2, mh, mx, a);
 }
@@ -769,11 +809,45 @@ nvfp4moe_status launch_fp8_layer(const Fp8LayerCall& c, cudaStream_t s) {
   if (st != NVFP4MOE_OK) return st;
   fp8_layer_prepare_kernel<<<(c.T * a.nH * 8 + 255) / 256, 256, 0, s>>>(
       static_cast<const __nv_bfloat16*>(c.x), c.T, c.H, c.x_codes, c.x_scale, c.counters, touched + kMaxParts + 1);
-  const size_t smem = smem_layout(nt, a.nH, c.k, c.E, a.stages).total;
+  const size_t smem = smem_layout(nt, a.nH, c.k, c.E, a.stages, false).total;
   const cudaError_t e = nt == 16 ? launch_columns<16>(m13, m2, mh, mx, a, num_sms(), smem, s)
                                  : launch_columns<32>(m13, m2, mh, mx, a, num_sms(), smem, s);
   if (e != cudaSuccess) return fail(NVFP4MOE_CUDA_ERROR, "fp8 layer: %s", cudaGetErrorString(e));
   return check_launch("fp8 layer");
+}
+
+// Rows a unit takes: the groups of an expert that gets `rows` on average should mostly be one.
+int fp8_stream_rows(int64_t pairs, int E) {
+  const int64_t touched = pairs < E ? pairs : E;
+  const int64_t mean = touched > 0 ? pairs / touched : 0;
+  return mean <= 20 ? 32 : (mean <= 44 ? 64 : 0);
+}
+
+nvfp4moe_status launch_fp8_stream(const GroupedArgs& g, int nt, int* counters, cudaStream_t s) {
+  LayerArgs a{};
+  a.x_scale = g.x_scale;
+  a.list = g.tiles;
+  a.H = g.H, a.I = g.I, a.E = g.E;
+  a.nH = int(fp8_blocks(g.H)), a.nI = int(fp8_blocks(g.I));
+  for (a.stages = kMaxStages; smem_layout(nt, 0, 0, 0, a.stages, true).total > kSmemLimit; --a.stages) {
+  }
+  if (a.stages > slots_of(nt)) a.stages = slots_of(nt);  // see the scale warps
+  a.w13_scale = g.w13_scale, a.w2_scale = g.w2_scale;
+  a.h_codes = g.h_codes, a.h_scale = g.h_scale, a.slots = g.slots;
+  a.done = counters;
+  a.status = device_status_ptr();
+  if (!a.status) return fail(NVFP4MOE_CUDA_ERROR, "device status word unavailable");
+  CUtensorMap m13, m2, mh, mx;
+  nvfp4moe_status st = make_fp8_map(&m13, g.w13_codes, g.H, g.I, 2 * int64_t(g.E), g.H, int64_t(g.I) * g.H, 128);
+  if (st == NVFP4MOE_OK) st = make_fp8_map(&m2, g.w2_codes, g.I, g.H, g.E, g.I, int64_t(g.I) * g.H, 128);
+  if (st == NVFP4MOE_OK) st = make_fp8_map(&mh, g.h_codes, g.I, g.rows, 1, g.I, g.I, nt);
+  if (st == NVFP4MOE_OK) st = make_fp8_map(&mx, g.x_codes, g.H, g.rows, 1, g.H, g.H, nt);
+  if (st != NVFP4MOE_OK) return st;
+  const size_t smem = smem_layout(nt, 0, 0, 0, a.stages, true).total;
+  const cudaError_t e = nt == 32 ? launch_one<32, 1, true>(m13, m2, mh, mx, a, num_sms(), smem, s)
+                                 : launch_one<64, 1, true>(m13, m2, mh, mx, a, num_sms(), smem, s);
+  if (e != cudaSuccess) return fail(NVFP4MOE_CUDA_ERROR, "fp8 stream: %s", cudaGetErrorString(e));
+  return check_launch("fp8 stream");
 }
 
 }  // namespace nvfp4moe

@@ -81,6 +81,12 @@ struct Fp8LayerCall {
   float* x_scale;
   void* out;
 };
+// The same stream over rows in expert order, for batches whose experts get few rows each: units of at
+// most fp8_stream_rows rows (0: too many rows an expert, launch_fp8_grouped is the way).  g.tiles lists
+// groups of that many rows; counters: as many ints as groups, zero.
+int fp8_stream_rows(int64_t pairs, int E);
+nvfp4moe_status launch_fp8_stream(const GroupedArgs& g, int rows, int* counters, cudaStream_t s);
+
 bool fp8_layer_fits(int T, int H, int I, int E, int k);
 Fp8LayerSizes fp8_layer_sizes(int T, int H, int I, int E, int k);
 nvfp4moe_status launch_fp8_layer(const Fp8LayerCall& c, cudaStream_t s);
