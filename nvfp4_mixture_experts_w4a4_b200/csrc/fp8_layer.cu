@@ -22,7 +22,7 @@
 // token, in slot order, and rounds once.
 //
 // GROUPED is the same stream for larger batches whose experts get few rows each: the routing and x in
-// expert order come from launches before, units take at most NT rows of an expert, x comes per stage
+// expert order come from launches before, units take at most 32 rows of an expert, x comes per stage
 // as h does, and the rows of the output stay in expert order for the combine's own launch.
 //
 // Warps: 0 streams weights (TMA); 1 owns TMEM and issues the MMAs; 2 and 3 fetch x and its scales;
@@ -45,7 +45,7 @@ constexpr int kThreads = 512;
 constexpr int kTile = 128 * 128;         // bytes of a weight tile
 constexpr int kStage = 2 * kTile;
 constexpr int kMaxStages = 6, kMinStages = 3;  // (more than 8 or less than 3: see the scale warps)
-constexpr int slots_of(int nt) { return nt == 64 ? 4 : 8; }  // accumulator slots (stages past the MMA)
+constexpr int kSlots = 8;                // accumulator slots (stages in flight past the MMA)
 constexpr int kMaxE = 1024;
 constexpr int kPitch = 132;              // floats of a row of the exchange buffer
 constexpr int kSmemLimit = 226 * 1024;   // dynamic; a few hundred bytes more are static
@@ -93,8 +93,8 @@ __host__ __device__ inline Smem smem_layout(int nt, int nH, int k, int E, int st
   m.h = put(stages * 2 * nt * 128);
   m.x = put(nH * nt * 128);
   m.xs = put(nH * nt * 4);
-  m.sb = put(slots_of(nt) * 2 * 4);
-  m.hs = put(slots_of(nt) * 2 * nt * 4);
+  m.sb = put(kSlots * 2 * 4);
+  m.hs = put(kSlots * 2 * nt * 4);
   m.buf = put(nt * kPitch * 4);
   const int most = nt * k < E ? nt * k : E;
   m.mask = put(E * 4);
@@ -103,7 +103,7 @@ __host__ __device__ inline Smem smem_layout(int nt, int nH, int k, int E, int st
   m.row0 = put((most + 1) * 4);
   m.ids = put(nt * k * 4);
   m.w = put(nt * k * 4);
-  m.bars = put((2 * kMaxStages + 2 * slots_of(nt) + 4) * 8);
+  m.bars = put((2 * kMaxStages + 2 * kSlots + 4) * 8);
   m.total = at + 1024;
   return m;
 }
@@ -291,7 +291,6 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_shared_1024(smem_raw);
   const Smem m = smem_layout(NT, a.nH, a.k, a.E, a.stages, GROUPED);
-  constexpr int kSlots = slots_of(NT);
   float* s_xs = reinterpret_cast<float*>(smem + m.xs);          // [nH][NT]
   float* s_sb = reinterpret_cast<float*>(smem + m.sb);          // [slot][2]
   float* s_hs = reinterpret_cast<float*>(smem + m.hs);          // [slot][2][NT]
@@ -816,14 +815,8 @@ nvfp4moe_status launch_fp8_layer(const Fp8LayerCall& c, cudaStream_t s) {
   return check_launch("fp8 layer");
 }
 
-// Rows a unit takes: the groups of an expert that gets `rows` on average should mostly be one.
-int fp8_stream_rows(int64_t pairs, int E) {
-  const int64_t touched = pairs < E ? pairs : E;
-  const int64_t mean = touched > 0 ? pairs / touched : 0;
-  return mean <= 20 ? 32 : (mean <= 44 ? 64 : 0);
-}
-
-nvfp4moe_status launch_fp8_stream(const GroupedArgs& g, int nt, int* counters, cudaStream_t s) {
+nvfp4moe_status launch_fp8_stream(const GroupedArgs& g, int* counters, cudaStream_t s) {
+  constexpr int nt = kStreamRows;
   LayerArgs a{};
   a.x_scale = g.x_scale;
   a.list = g.tiles;
@@ -831,9 +824,8 @@ nvfp4moe_status launch_fp8_stream(const GroupedArgs& g, int nt, int* counters, c
   a.nH = int(fp8_blocks(g.H)), a.nI = int(fp8_blocks(g.I));
   for (a.stages = kMaxStages; smem_layout(nt, 0, 0, 0, a.stages, true).total > kSmemLimit; --a.stages) {
   }
-  if (a.stages > slots_of(nt)) a.stages = slots_of(nt);  // see the scale warps
   a.w13_scale = g.w13_scale, a.w2_scale = g.w2_scale;
-  a.h_codes = g.h_codes, a.h_scale = g.h_scale, a.slots = g.slots;
+  a.h_codes = g.h_codes, a.h_scale = g.h_scale, a.slots = static_cast<float*>(g.slots);
   a.done = counters;
   a.status = device_status_ptr();
   if (!a.status) return fail(NVFP4MOE_CUDA_ERROR, "device status word unavailable");
@@ -844,8 +836,7 @@ nvfp4moe_status launch_fp8_stream(const GroupedArgs& g, int nt, int* counters, c
   if (st == NVFP4MOE_OK) st = make_fp8_map(&mx, g.x_codes, g.H, g.rows, 1, g.H, g.H, nt);
   if (st != NVFP4MOE_OK) return st;
   const size_t smem = smem_layout(nt, 0, 0, 0, a.stages, true).total;
-  const cudaError_t e = nt == 32 ? launch_one<32, 1, true>(m13, m2, mh, mx, a, num_sms(), smem, s)
-                                 : launch_one<64, 1, true>(m13, m2, mh, mx, a, num_sms(), smem, s);
+  const cudaError_t e = launch_one<nt, 1, true>(m13, m2, mh, mx, a, num_sms(), smem, s);
   if (e != cudaSuccess) return fail(NVFP4MOE_CUDA_ERROR, "fp8 stream: %s", cudaGetErrorString(e));
   return check_launch("fp8 stream");
 }

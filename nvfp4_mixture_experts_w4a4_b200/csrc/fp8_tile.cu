@@ -50,10 +50,14 @@ constexpr int SC_FLOATS = SC_BLOCKS * 2 * TM;   // [block][half][row]
 
 // rows of B a CTA holds per stage, stages, and shared memory
 constexpr int b_rows(int bn, bool pair) { return pair ? bn / 2 : bn; }
-constexpr int stages_of(int bn, bool pair) { return b_rows(bn, pair) == 256 ? 4 : 6; }
-constexpr int ring_bytes(int bn, bool pair) { return stages_of(bn, pair) * (A_STAGE + b_rows(bn, pair) * TK); }
-constexpr int smem_bytes(int bn, bool pair) {
-  return 1024 + ring_bytes(bn, pair) + (2 * stages_of(bn, pair) + 2 * (512 / bn) + 5) * 8 + 16 + 2 * 2 * TM * 4 + 2 * SC_FLOATS * 4;
+constexpr int stages_of(int mode, int bn, bool pair) { return mode == DOWN ? 3 : (b_rows(bn, pair) == 256 ? 4 : 6); }
+constexpr int OUT_BLOCK = 32 * 128;  // down: 32 rows x 64 columns of fp16, one a warp, on their way out
+constexpr int ring_bytes(int mode, int bn, bool pair) {
+  return stages_of(mode, bn, pair) * (A_STAGE + b_rows(bn, pair) * TK) + (mode == DOWN ? ADD_WARPS * OUT_BLOCK : 0);
+}
+constexpr int smem_bytes(int mode, int bn, bool pair) {
+  return 1024 + ring_bytes(mode, bn, pair) + (2 * stages_of(mode, bn, pair) + 2 * (512 / bn) + 5) * 8 + 16 +
+         2 * 2 * TM * 4 + 2 * SC_FLOATS * 4;
 }
 constexpr int split_pitch(int bn) { return bn + 4; }  // floats; rows 16 bytes apart in the banks
 
@@ -174,6 +178,12 @@ __device__ __forceinline__ void store_32b(void* p, const uint32_t (&r)[8]) {
                : "memory");
 }
 
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -225,8 +235,9 @@ __device__ __forceinline__ Tile tile_of(const TileParams& p, int t, int bn, bool
 
 template <int MODE, int BN, bool SPLIT, bool PAIR>
 __global__ void __launch_bounds__(TTHREADS, 1)
-fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const TileParams p) {
-  constexpr int STAGES = stages_of(BN, PAIR);
+fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                const __grid_constant__ CUtensorMap tmD, const TileParams p) {
+  constexpr int STAGES = stages_of(MODE, BN, PAIR);
   constexpr int B_ROWS = b_rows(BN, PAIR);
   constexpr int B_STAGE = B_ROWS * TK;
   static_assert(!PAIR || (BN == 256 && !SPLIT), "a pair runs 256 x 256 tiles, whole sums");
@@ -238,7 +249,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   uint8_t* smem = align_shared_1024(smem_raw);
   uint8_t* sA = smem;
   uint8_t* sB = sA + STAGES * A_STAGE;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring_bytes(BN, PAIR));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring_bytes(MODE, BN, PAIR));
   uint64_t* empty = full + STAGES;
   uint64_t* acc_full = empty + STAGES;  // [NACC]
   uint64_t* acc_empty = acc_full + NACC;
@@ -272,6 +283,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tmA);
     prefetch_tensormap(&tmB);
+    if constexpr (MODE == DOWN) prefetch_tensormap(&tmD);
   }
   griddep_wait();  // the operands may come from the launch before
   griddep_launch_dependents();
@@ -292,14 +304,18 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   const int n_tiles = (GROUPED ? p.tiles[0].x : p.n_mt) * p.n_nt;
   constexpr int CTAS = PAIR ? 2 : 1;
   const int t_first = int(blockIdx.x) / (ranks * CTAS), t_step = int(gridDim.x) / (ranks * CTAS);
+  // a grouped tile comes from the list in memory, so each role reads one tile ahead
+  auto tile_at = [&](int t) { return t < n_tiles ? tile_of<PAIR>(p, t, BN, GROUPED) : Tile{0, 0, 1, 0}; };
   auto rows_of = [&](const Tile& w, int sd) { return max(0, min(TM, w.rows - sd * TM)); };
 
   if (warp < 4) {
     reg_give<40>();
     if (warp == 0 && elect_one()) {
       uint32_t it = 0;
+      Tile next = tile_at(t_first);
       for (int t = t_first; t < n_tiles && !*abort_flag; t += t_step) {
-        const Tile w = tile_of<PAIR>(p, t, BN, GROUPED);
+        const Tile w = next;
+        next = tile_at(t + t_step);
         const int boxes = (rows_of(w, side) + p.a_box - 1) / p.a_box;
         const int all_boxes = PAIR ? boxes + (rows_of(w, side ^ 1) + p.a_box - 1) / p.a_box : boxes;
         for (int kb = kb0; kb < kb1; ++kb, ++it) {
@@ -359,8 +375,10 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       // the products of both scales for SC_BLOCKS blocks at a time: a lane takes rows l and l + 64
       const int l = (warp - 2) * 32 + lane;
       uint32_t batch = 0;
+      Tile next = tile_at(t_first);
       for (int t = t_first; t < n_tiles && !*abort_flag; t += t_step) {
-        const Tile w = tile_of<PAIR>(p, t, BN, GROUPED);
+        const Tile w = next;
+        next = tile_at(t + t_step);
         const float* sa[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -409,7 +427,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     uint32_t it = 0, batch = 0;
     int done = 0;
     for (int t = t_first; t < n_tiles && !*abort_flag; t += t_step, ++done) {
-      const Tile pair_tile = tile_of<PAIR>(p, t, BN, GROUPED);
+      const Tile pair_tile = tile_at(t);
       Tile w = pair_tile;  // this CTA's rows of it
       w.row += side * TM;
       w.rows = rows_of(pair_tile, side);
@@ -527,6 +545,51 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             }
           }
         }
+      } else if constexpr (MODE == DOWN) {
+        // The row's 128 columns in fp16, times a power of two that brings the largest to [2^14, 2^15):
+        // half the bytes of fp32 rows, twice (written here, read by the combine), for 2^-11 of a
+        // value, an eighth of the output's own rounding to bf16.
+        const int n = w.n0 + half * HALF;
+        if (live && n < p.N) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int i = 0; i < HALF; ++i) m = max(m, abs_bits(acc[i]));
+          // (no scaling for zero, infinite and NaN rows; 2^126 at most)
+          const int up = m == 0u || m >= 0x7F800000u ? 0 : min(126, 141 - int(m >> 23));
+          const float f = __uint_as_float(uint32_t(127 + up) << 23);
+          if (r < w.rows) p.d_scale[int64_t(w.row + r) * p.ldd_s + n / TK] = __uint_as_float(uint32_t(127 - up) << 23);
+          uint8_t* out = smem + STAGES * (A_STAGE + B_STAGE) + (warp - 4) * OUT_BLOCK;
+          const bool whole = q * 32 + 32 <= w.rows;  // the rows after the last are another tile's
+#pragma unroll
+          for (int c = 0; c < HALF; c += 64) {
+            uint4 o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float* v = acc + c + 8 * i;
+              o[i] = make_uint4(f16x2(v[0] * f, v[1] * f), f16x2(v[2] * f, v[3] * f), f16x2(v[4] * f, v[5] * f),
+                                f16x2(v[6] * f, v[7] * f));
+            }
+            if (whole) {
+              // through shared memory and a tile store: 128 bytes of a row at a time (a lane storing its
+              // own row takes a turn for every 32 bytes: 7000 cycles a tile in fp32)
+              bulk_wait_group_read<0>();
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(out + lane * 128 + ((i ^ (lane & 7)) << 4)) = o[i];
+              fence_proxy_async_shared();
+              __syncwarp();
+              if (lane == 0 && n + c < p.N) {
+                tma_store_2d(&tmD, n + c, w.row + q * 32, out);
+                bulk_commit_group();
+              }
+            } else if (r < w.rows) {
+              uint16_t* d = static_cast<uint16_t*>(p.D) + int64_t(w.row + r) * p.ldd + n + c;
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (n + c + 8 * i < p.N) *reinterpret_cast<uint4*>(d + 8 * i) = o[i];  // N is a multiple of 16
+            }
+          }
+        }
       } else {
         const int n = w.n0 + half * HALF;
         if (!p.d_vec) {
@@ -595,6 +658,8 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     }
   }
 
+  if constexpr (MODE == DOWN)
+    if (warp >= 4 && lane == 0) bulk_wait_group<0>();  // the last rows are out
   tc_fence_before();
   __syncthreads();
   // a pair leaves together: each CTA's shared memory and barriers are used by the other
@@ -647,14 +712,15 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 }
 
 template <int MODE, int BN, bool SPLIT, bool PAIR>
-cudaError_t launch_tiles(const CUtensorMap& a, const CUtensorMap& b, const TileParams& p, int grid, cudaStream_t s) {
+cudaError_t launch_tiles(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& d, const TileParams& p, int grid,
+                         cudaStream_t s) {
   constexpr auto kern = fp8_tile_kernel<MODE, BN, SPLIT, PAIR>;
-  cudaError_t e = set_smem_limit_once<kern>(smem_bytes(BN, PAIR));
+  cudaError_t e = set_smem_limit_once<kern>(smem_bytes(MODE, BN, PAIR));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(TTHREADS);
-  cfg.dynamicSmemBytes = smem_bytes(BN, PAIR);
+  cfg.dynamicSmemBytes = smem_bytes(MODE, BN, PAIR);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   int n = 0;
@@ -672,7 +738,7 @@ cudaError_t launch_tiles(const CUtensorMap& a, const CUtensorMap& b, const TileP
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, kern, a, b, p);
+  return cudaLaunchKernelEx(&cfg, kern, a, b, d, p);
 }
 
 }  // namespace
@@ -706,11 +772,11 @@ int resident_clusters(int split) {
     if (const int v = known[dev][split].load(std::memory_order_relaxed)) return v;
   constexpr auto kern = fp8_tile_kernel<DENSE, BN, true, false>;
   int n = 0;
-  if (set_smem_limit_once<kern>(smem_bytes(BN, false)) == cudaSuccess) {
+  if (set_smem_limit_once<kern>(smem_bytes(DENSE, BN, false)) == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(num_sms() / split * split));
     cfg.blockDim = dim3(TTHREADS);
-    cfg.dynamicSmemBytes = smem_bytes(BN, false);
+    cfg.dynamicSmemBytes = smem_bytes(DENSE, BN, false);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = split;
@@ -726,6 +792,25 @@ int resident_clusters(int split) {
   }
   if (dev >= 0 && dev < 64) known[dev][split].store(n, std::memory_order_relaxed);
   return n;
+}
+
+}  // namespace
+
+namespace {
+
+// fp16 [rows][H], box 64 columns x 32 rows, 128-byte swizzle; stores past the last column are clipped.
+nvfp4moe_status make_f16_rows_map(CUtensorMap* map, void* base, int64_t rows, int64_t H) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return fail(NVFP4MOE_CUDA_ERROR, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint64_t dims[2] = {cuuint64_t(H), cuuint64_t(rows)};
+  const cuuint64_t strides[1] = {cuuint64_t(H * 2)};
+  const cuuint32_t box[2] = {64u, 32u};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(NVFP4MOE_CUDA_ERROR, "cuTensorMapEncodeTiled (fp16 rows) failed (%d)", int(r));
+  return NVFP4MOE_OK;
 }
 
 }  // namespace
@@ -786,13 +871,13 @@ nvfp4moe_status launch_fp8_dense(const uint8_t* A, int64_t lda, const float* A_s
   const int grid = plan.split > 1 ? int(tiles * ctas) : int(tiles < resident ? tiles : resident) * ctas;
   cudaError_t e;
   if (plan.pair)
-    e = launch_tiles<DENSE, 256, false, true>(am, bm, p, grid, s);
+    e = launch_tiles<DENSE, 256, false, true>(am, bm, bm, p, grid, s);
   else if (plan.bn == 256)
-    e = plan.split > 1 ? launch_tiles<DENSE, 256, true, false>(am, bm, p, grid, s)
-                       : launch_tiles<DENSE, 256, false, false>(am, bm, p, grid, s);
+    e = plan.split > 1 ? launch_tiles<DENSE, 256, true, false>(am, bm, bm, p, grid, s)
+                       : launch_tiles<DENSE, 256, false, false>(am, bm, bm, p, grid, s);
   else
-    e = plan.split > 1 ? launch_tiles<DENSE, 128, true, false>(am, bm, p, grid, s)
-                       : launch_tiles<DENSE, 128, false, false>(am, bm, p, grid, s);
+    e = plan.split > 1 ? launch_tiles<DENSE, 128, true, false>(am, bm, bm, p, grid, s)
+                       : launch_tiles<DENSE, 128, false, false>(am, bm, bm, p, grid, s);
   if (e != cudaSuccess) return fail(NVFP4MOE_CUDA_ERROR, "fp8_gemm: %s", cudaGetErrorString(e));
   return check_launch("fp8_gemm");
 }
@@ -801,12 +886,14 @@ nvfp4moe_status launch_fp8_grouped(const GroupedArgs& g, cudaStream_t s) {
   uint32_t* status = device_status_ptr();
   if (!status) return fail(NVFP4MOE_CUDA_ERROR, "device status word unavailable");
   const int nI = int(fp8_blocks(g.I)), nH = int(fp8_blocks(g.H));
-  CUtensorMap xm, w13, hm, w2;
+  CUtensorMap xm, w13, hm, w2, dm;
   nvfp4moe_status st = make_fp8_map(&xm, g.x_codes, g.H, g.rows, 1, g.H, g.H, 32);
   if (st == NVFP4MOE_OK)
     st = make_fp8_map(&w13, g.w13_codes, g.H, g.I, 2 * int64_t(g.E), g.H, int64_t(g.I) * g.H, TM);
   if (st == NVFP4MOE_OK) st = make_fp8_map(&hm, g.h_codes, g.I, g.rows, 1, g.I, g.I, 32);
   if (st == NVFP4MOE_OK) st = make_fp8_map(&w2, g.w2_codes, g.I, g.H, g.E, g.I, int64_t(g.I) * g.H, 256);
+  if (st != NVFP4MOE_OK) return st;
+  if (st == NVFP4MOE_OK) st = make_f16_rows_map(&dm, g.slots, g.rows, g.H);
   if (st != NVFP4MOE_OK) return st;
   TileParams p{};
   p.a_box = 32;
@@ -821,15 +908,15 @@ nvfp4moe_status launch_fp8_grouped(const GroupedArgs& g, cudaStream_t s) {
   p.h_codes = g.h_codes, p.ldh = g.I, p.h_scale = g.h_scale, p.ldh_s = nI;
   const int64_t most = int64_t(g.max_row_tiles) * nI;
   const int grid1 = int(most < num_sms() ? most : num_sms());
-  cudaError_t e = launch_tiles<GATEUP, 256, false, false>(xm, w13, p, grid1, s);
-  // down: fp32 rows in expert order
+  cudaError_t e = launch_tiles<GATEUP, 256, false, false>(xm, w13, w13, p, grid1, s);
+  // down: fp16 rows and their scales in expert order
   p.nkb = nI, p.n_nt = int((g.H + 255) / 256), p.nsb = nH, p.N = g.H;
   p.sa = g.h_scale, p.lda_s = nI;
   p.sb = g.w2_scale, p.ldb_s = nI, p.sb_e = int64_t(nH) * nI;
-  p.D = g.slots, p.ldd = g.H, p.d_f32 = 1, p.d_vec = 1;
+  p.D = g.slots, p.ldd = g.H, p.d_scale = g.slot_scale, p.ldd_s = nH;
   const int64_t most2 = int64_t(g.max_row_tiles) * p.n_nt;
   const int grid2 = int(most2 < num_sms() ? most2 : num_sms());
-  if (e == cudaSuccess) e = launch_tiles<DOWN, 256, false, false>(hm, w2, p, grid2, s);
+  if (e == cudaSuccess) e = launch_tiles<DOWN, 256, false, false>(hm, w2, dm, p, grid2, s);
   if (e != cudaSuccess) return fail(NVFP4MOE_CUDA_ERROR, "fp8 grouped products: %s", cudaGetErrorString(e));
   return check_launch("fp8 grouped products");
 }

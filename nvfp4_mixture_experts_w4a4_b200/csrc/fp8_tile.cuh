@@ -21,6 +21,8 @@ struct TileParams {
   void* D;
   int64_t ldd;
   int d_f32, d_vec;
+  float* d_scale;            // down: D is fp16, its value times d_scale[row * ldd_s + column / 128]
+  int64_t ldd_s;
   uint8_t* h_codes;          // gate/up: h in E4M3, rows of A
   float* h_scale;
   int64_t ldh, ldh_s;
@@ -39,7 +41,7 @@ nvfp4moe_status launch_fp8_dense(const uint8_t* A, int64_t lda, const float* A_s
                                  int64_t ldb, const float* B_scale, int64_t ldb_s, int64_t M, int64_t N, int64_t K,
                                  void* D, int64_t ldd, int d_f32, cudaStream_t s);
 
-// Gate/up (SwiGLU, h in E4M3) then down (fp32 rows) over the rows of x in expert order.
+// Gate/up (SwiGLU, h in E4M3) then down over the rows of x in expert order.
 struct GroupedArgs {
   int H, I, E;
   int64_t rows;              // rows of x_codes, h_codes and slots
@@ -53,7 +55,8 @@ struct GroupedArgs {
   const float* w2_scale;     // [E][H / 128][I / 128]
   uint8_t* h_codes;          // [rows][I]
   float* h_scale;            // [rows][I / 128]
-  float* slots;              // [rows][H]
+  void* slots;               // [rows][H]: fp32 (launch_fp8_stream), or fp16 with slot_scale (launch_fp8_grouped)
+  float* slot_scale;         // [rows][H / 128]
 };
 nvfp4moe_status launch_fp8_grouped(const GroupedArgs& g, cudaStream_t s);
 
@@ -81,11 +84,10 @@ struct Fp8LayerCall {
   float* x_scale;
   void* out;
 };
-// The same stream over rows in expert order, for batches whose experts get few rows each: units of at
-// most fp8_stream_rows rows (0: too many rows an expert, launch_fp8_grouped is the way).  g.tiles lists
-// groups of that many rows; counters: as many ints as groups, zero.
-int fp8_stream_rows(int64_t pairs, int E);
-nvfp4moe_status launch_fp8_stream(const GroupedArgs& g, int rows, int* counters, cudaStream_t s);
+// The same stream over rows in expert order, for batches whose experts get few rows each: g.tiles
+// lists groups of at most kStreamRows rows; counters: as many zeros as groups.
+constexpr int kStreamRows = 32;
+nvfp4moe_status launch_fp8_stream(const GroupedArgs& g, int* counters, cudaStream_t s);
 
 bool fp8_layer_fits(int T, int H, int I, int E, int k);
 Fp8LayerSizes fp8_layer_sizes(int T, int H, int I, int E, int k);

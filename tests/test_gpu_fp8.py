@@ -253,7 +253,13 @@ def experts(E, I, H, seed):
     return ops.FP8Experts.from_float(*w, torch.randn(E, H, I, generator=g, device="cuda") / math.sqrt(I))
 
 
-def layer_reference(w, x, logits, k):
+def in_tiles(T, E, k, launch=C.LAUNCH_AUTO):
+    """Whether a batch runs in row tiles, whose rows of the output wait for the combine in fp16."""
+    P = T * k
+    return (T > 32 or launch == C.LAUNCH_MULTI) and (T > 256 or P > 20 * min(P, E))
+
+
+def layer_reference(w, x, logits, k, tiles):
     """(out, bound) in 64 bits.  The kernels' gate and up sums differ from the real ones by at most
     eg = (4 * 128 + nkb + 2) 2^-24 of the sums of magnitudes; silu (slope at most 1.1) and its fast
     exponential and division add 2^-18 of h, so h is off by at most
@@ -263,7 +269,8 @@ def layer_reference(w, x, logits, k):
     error; it differs by the grid's step there (at most |code| / 8, or 2^-9), or a scale that rounds
     elsewhere moves the dequantised value by its relative change.  The output is off by those, weighted
     by the down weights and the routing, by the product's own bound, by the softmax's 2^-21 and by half
-    a step of bf16."""
+    a step of bf16; and where rows wait in fp16, by half a step of it, 2^-11 of the value or, for those below
+    2^-28 of the largest in 128 columns (which is scaled to 2^14 or more), 2^-25 / 2^14 of that."""
     T, E = logits.shape
     H, I = w.H, w.I
     lg = logits.double()
@@ -299,12 +306,13 @@ def layer_reference(w, x, logits, k):
         size = (hq * S).abs() @ wd.abs().T
         c = p[t, j][:, None]
         out.index_add_(0, t, c * y)
-        bound.index_add_(0, t, c * (dh @ wd.abs().T + (es(I) + 2.0 ** -21 + k * 2.0 ** -24) * size))
+        slot = 2.0 ** -11 * (y.abs() + es(I) * size) + 2.0 ** -39 * y.abs().amax(1, keepdim=True) if tiles else 0.0
+        bound.index_add_(0, t, c * (dh @ wd.abs().T + (es(I) + 2.0 ** -21 + k * 2.0 ** -24) * size + slot))
     return out, bound * (1 + BF16_HALF) + BF16_HALF * out.abs()
 
 
-def check_layer(w, x, logits, k, y):
-    ref, bound = layer_reference(w, x, logits, k)
+def check_layer(w, x, logits, k, y, launch=C.LAUNCH_AUTO):
+    ref, bound = layer_reference(w, x, logits, k, in_tiles(*logits.shape, k, launch))
     err = (y.double() - ref).abs()
     assert (err <= bound).all(), (err / bound.clamp(min=1e-300)).max()
 
@@ -314,7 +322,8 @@ CASES = [
     (1, 256, 128, 8, 2), (1, 2048, 512, 64, 10), (1, 1024, 4096, 1, 1), (2, 16, 16, 3, 3), (3, 144, 80, 5, 1),
     (8, 256, 128, 8, 2), (15, 1040, 336, 20, 3), (16, 512, 256, 512, 10), (16, 400, 144, 1024, 32), (17, 768, 384, 12, 4),
     (32, 2048, 128, 40, 8), (32, 256, 128, 1, 1), (33, 256, 128, 8, 2), (45, 1040, 336, 20, 3), (130, 640, 208, 7, 2),
-    (300, 384, 512, 3, 1), (600, 272, 128, 300, 5), (16, 7168, 128, 6, 2), (5, 6144, 256, 4, 2),
+    (300, 384, 512, 3, 1), (600, 272, 128, 300, 5), (16, 7168, 128, 6, 2), (5, 6144, 256, 4, 2), (256, 640, 208, 64, 5),
+    (257, 640, 208, 64, 5), (90, 1040, 656, 3, 1), (700, 1552, 96, 5, 2), (1500, 256, 128, 1, 1),
 ]
 
 
@@ -348,7 +357,7 @@ def test_layer_launches(T, launch):
             logits[:] = 0.25
         if seed == 3:      # one token alone among the others' experts
             logits[0] = -logits[0]
-        check_layer(w, x, logits, 4, layer(x, logits))
+        check_layer(w, x, logits, 4, layer(x, logits), launch)
     assert ops.device_status() == 0
 
 
@@ -365,6 +374,17 @@ def test_layer_rows_stay_apart(T):
     others = torch.tensor([t for t in range(T) if t not in (2, 5, 7)], device="cuda")
     assert torch.equal(y[others], clean[others])
     assert y[2].isnan().all() and not y[5].isfinite().any() and (y[7] == 0).all()
+
+
+def test_layer_rows_of_any_size():
+    """Rows that wait in fp16 keep their precision whatever their size: down weights from 2^-100 to 2^100."""
+    T, H, I = 300, 256, 128
+    g = gen(4)
+    x, logits = torch.randn(T, H, generator=g, device="cuda").bfloat16(), torch.zeros(T, 1, device="cuda")
+    w = experts(1, I, H, 7)
+    for e in (-100, -20, 0, 20, 100):
+        v = ops.FP8Experts(w.w13_codes, w.w13_scale, w.w2_codes, w.w2_scale * 2.0 ** e)
+        check_layer(v, x, logits, 1, ops.FP8MoeFFN(v, 1)(x, logits))
 
 
 def test_layer_inputs_and_outputs():
