@@ -260,10 +260,16 @@ nvfp4moe_status fp8_moe_ffn_forward(const fp8_moe_ffn_desc* desc, const void* x,
     c.x_codes = ws + L.x_codes, c.x_scale = f32(L.x_scale);
     return launch_fp8_layer(c, s);
   }
-  st = launch_batch_prologue(x, logits, d.T, d.H, d.E, d.top_k, 1, 0, nullptr, i32(L.ids), f32(L.w), i32(L.counts),
-                             i32(L.offsets), i32(L.padded), i32(L.pair_to_row), i32(L.row_token), i32(L.row_pair),
-                             i32(L.tile_expert), i32(L.active), nullptr, 1, nullptr, nullptr, ws + L.scratch, nullptr,
-                             nullptr, s);
+  // routing and permutation: one cluster launch for the batches that it takes, else three over slices
+  if (prologue_fits(d.T, d.E, d.top_k))
+    st = launch_prologue(x, logits, d.T, d.H, d.E, d.top_k, 1, 0, nullptr, i32(L.ids), f32(L.w), i32(L.counts),
+                         i32(L.offsets), i32(L.padded), i32(L.pair_to_row), i32(L.row_token), i32(L.row_pair),
+                         i32(L.tile_expert), i32(L.active), nullptr, 1, nullptr, nullptr, nullptr, nullptr, 0, 0, s);
+  else
+    st = launch_batch_prologue(x, logits, d.T, d.H, d.E, d.top_k, 1, 0, nullptr, i32(L.ids), f32(L.w), i32(L.counts),
+                               i32(L.offsets), i32(L.padded), i32(L.pair_to_row), i32(L.row_token), i32(L.row_pair),
+                               i32(L.tile_expert), i32(L.active), nullptr, 1, nullptr, nullptr, ws + L.scratch, nullptr,
+                               nullptr, s);
   if (st != NVFP4MOE_OK) return st;
   int4* tiles = reinterpret_cast<int4*>(ws + L.tiles);
   const int64_t groups = int64_t(d.T) * fp8_blocks(d.H);
