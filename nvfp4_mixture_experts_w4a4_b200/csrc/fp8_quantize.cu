@@ -1,8 +1,7 @@
 // fp8_quantize: bf16 / fp32 -> E4M3 with one fp32 scale per 1 x 128 or 128 x 128 group.
 //
 // Each element is read once and each code written once, so the bound is memory: 3 (bf16) or 5
-// (fp32) bytes an element.  A row group is held by eight lanes (16 elements each: fewer lanes leave the shuffles,
-// the scale and the addresses to fewer instructions an element), two groups in flight a lane.  A
+// (fp32) bytes an element.  A row group is held by a few lanes with 64 bytes or 128 in flight each.  A
 // square block is held in the registers of one CTA (64 elements a thread), so it too is read once.
 // Rows whose start, pitch or length does not allow 16-byte loads take scalar ones.
 #include "fp8.cuh"
@@ -98,64 +97,97 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int n, const uint32_t* w
 }
 
 constexpr int kThreads = 256;
-constexpr int kLanes = 8;  // lanes that hold a row group
+// Lanes that hold a row group, and groups of a lane, all loaded before the first is used.  Measured, TB/s at
+// 16384 x 16384 bf16 / 8 x 4096 x 4096 fp32: 4 lanes 5.5 / -, 8 lanes and one group 4.0 / 5.7, two groups
+// 4.8 / 6.4, 16 lanes - / 5.0 (fewer lanes: fewer instructions an element for the scale and the shuffles).
+template <typename T>
+constexpr int lanes_of() { return sizeof(T) == 2 ? 4 : 8; }
+template <typename T>
+constexpr int depth_of() { return sizeof(T) == 2 ? 1 : 2; }
 constexpr int kBlockThreads = 512;
 
-template <typename T, bool VECTOR>
+template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) fp8_rows_kernel(QuantArgs a) {
   constexpr int VEC = 16 / sizeof(T);                  // elements of a 16-byte load
+  constexpr int kLanes = lanes_of<T>();
   constexpr int CHUNKS = FP8_BLOCK / (VEC * kLanes);   // loads a lane and group: 2 (bf16), 4 (fp32)
-  constexpr int DEPTH = 2;                             // groups in flight a lane
+  constexpr int DEPTH = depth_of<T>();
   const int nb = int((a.K + FP8_BLOCK - 1) / FP8_BLOCK);
   const int64_t groups = a.rows * nb;
   const int sub = threadIdx.x % kLanes;
-  // this lane's groups: first, first + step, ...; (row, b) is the current one
-  const int64_t first = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / kLanes;
-  const int64_t step = int64_t(gridDim.x) * (kThreads / kLanes);
-  const int64_t step_rows = step / nb;
-  const int step_b = int(step - step_rows * nb);
+  // this lane's groups: first and first + half, half a CTA's share apart
+  const int64_t first = int64_t(blockIdx.x) * (DEPTH * kThreads / kLanes) + threadIdx.x / kLanes;
   const int K = int(a.K) - sub * VEC;  // elements of a row from this lane's first on
   for (int64_t bi = blockIdx.y; bi < a.batch; bi += gridDim.y) {
     const T* x = static_cast<const T*>(a.x) + bi * a.x_batch + sub * VEC;
     uint8_t* codes = a.codes + bi * a.c_batch + sub * VEC;
     float* scale = a.scale + bi * a.s_batch;
-    int64_t row = first / nb;
-    int b = int(first - row * nb);
-    // the lanes of a warp take the same turns (its last groups may not exist)
-    for (int64_t left = groups - (first - (threadIdx.x & 31) / kLanes); left > 0; left -= DEPTH * step) {
-      uint32_t u[DEPTH][CHUNKS][4];
-      int64_t rows[DEPTH];
-      int cs[DEPTH];
+    uint32_t u[DEPTH][CHUNKS][4];
+    int64_t rows[DEPTH];
+    int cs[DEPTH];
 #pragma unroll
-      for (int d = 0; d < DEPTH; ++d) {
-        rows[d] = row;
-        cs[d] = row < a.rows ? b * FP8_BLOCK : INT32_MAX / 2;  // past the row's end: nothing is read or written
-        const T* p = x + row * a.ldx + b * FP8_BLOCK;
+    for (int d = 0; d < DEPTH; ++d) {
+      const int64_t g = first + d * (kThreads / kLanes);
+      rows[d] = groups <= INT32_MAX ? int64_t(uint32_t(g) / uint32_t(nb)) : g / nb;
+      const int b = int(g - rows[d] * nb);
+      cs[d] = g < groups ? b * FP8_BLOCK : INT32_MAX / 2;  // past the row's end: nothing is read or written
+      const T* p = x + rows[d] * a.ldx + b * FP8_BLOCK;
 #pragma unroll
-        for (int j = 0; j < CHUNKS; ++j)
-          load_words<T, 4, VECTOR>(p + j * kLanes * VEC, K - cs[d] - j * kLanes * VEC, u[d][j]);
-        row += step_rows, b += step_b;
-        if (b >= nb) b -= nb, ++row;
+      for (int j = 0; j < CHUNKS; ++j)
+        load_words<T, 4, true>(p + j * kLanes * VEC, K - cs[d] - j * kLanes * VEC, u[d][j]);
+    }
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < CHUNKS; ++j) m = max(m, words_max<T, 4>(u[d][j]));
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const auto f = scale_for<T>(m);
+      uint8_t* q = codes + rows[d] * a.ldc + cs[d];
+#pragma unroll
+      for (int j = 0; j < CHUNKS; ++j) {
+        uint32_t w[VEC / 4];
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i) w[i] = encode_words<T>(u[d][j] + i * sizeof(T), f);
+        store_codes<VEC / 4, true>(q + j * kLanes * VEC, K - cs[d] - j * kLanes * VEC, w);
       }
+      if (sub == 0 && cs[d] < K) scale[rows[d] * a.lds + cs[d] / FP8_BLOCK] = f.scale;
+    }
+  }
+}
+
+// The same for rows that start anywhere: a warp takes a group, its lanes every 32nd element, so that
+// single loads and byte stores are still neighbours'.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) fp8_rows_any_kernel(QuantArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int nb = int((a.K + FP8_BLOCK - 1) / FP8_BLOCK);
+  const int64_t g = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / 32;
+  if (g >= a.rows * nb) return;  // whole warps
+  const int64_t row = g / nb;
+  const int c = int(g - row * nb) * FP8_BLOCK + lane;
+  for (int64_t bi = blockIdx.y; bi < a.batch; bi += gridDim.y) {
+    const T* x = static_cast<const T*>(a.x) + bi * a.x_batch + row * a.ldx;
+    float v[4];
+    uint32_t m = 0;
 #pragma unroll
-      for (int d = 0; d < DEPTH; ++d) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < CHUNKS; ++j) m = max(m, words_max<T, 4>(u[d][j]));
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const auto f = scale_for<T>(m);
-        uint8_t* q = codes + rows[d] * a.ldc + cs[d];
-#pragma unroll
-        for (int j = 0; j < CHUNKS; ++j) {
-          uint32_t w[VEC / 4];
-#pragma unroll
-          for (int i = 0; i < VEC / 4; ++i) w[i] = encode_words<T>(u[d][j] + i * sizeof(T), f);
-          store_codes<VEC / 4, VECTOR>(q + j * kLanes * VEC, K - cs[d] - j * kLanes * VEC, w);
-        }
-        if (sub == 0 && cs[d] < K) scale[rows[d] * a.lds + cs[d] / FP8_BLOCK] = f.scale;
+    for (int i = 0; i < 4; ++i) {
+      v[i] = 0.0f;
+      if (c + 32 * i < a.K) {
+        if constexpr (sizeof(T) == 2) v[i] = __bfloat162float(x[c + 32 * i]);
+        else v[i] = x[c + 32 * i];
       }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, abs_bits(v[i]));
+    const auto f = scale_for<T>(__reduce_max_sync(0xffffffffu, m));
+    const uint32_t w = fp8_encode4(v, f);
+    uint8_t* q = a.codes + bi * a.c_batch + row * a.ldc + c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + 32 * i < a.K) q[32 * i] = static_cast<uint8_t>(w >> (8 * i));
+    if (lane == 0) a.scale[bi * a.s_batch + row * a.lds + c / FP8_BLOCK] = f.scale;
   }
 }
 
@@ -201,13 +233,13 @@ __global__ void __launch_bounds__(kBlockThreads, 2) fp8_blocks_kernel(QuantArgs 
 
 template <typename T>
 void launch_rows(const QuantArgs& a, bool vec, cudaStream_t s) {
-  const int64_t per_block = kThreads / kLanes;
-  const int64_t want = (a.rows * fp8_blocks(a.K) + per_block - 1) / per_block;
-  const int64_t most = int64_t(num_sms()) * 8;  // eight CTAs an SM, then a grid-wide stride
-  const dim3 grid(static_cast<unsigned>(want < most ? want : most),
+  // no grid-wide stride: CTAs that finish early make room for the next ones, where a fixed grid's last
+  // turn was a third empty at 4096 x 5120
+  const int64_t per_block = vec ? depth_of<T>() * kThreads / lanes_of<T>() : kThreads / 32;
+  const dim3 grid(static_cast<unsigned>((a.rows * fp8_blocks(a.K) + per_block - 1) / per_block),
                   static_cast<unsigned>(a.batch < 65535 ? a.batch : 65535));
-  if (vec) fp8_rows_kernel<T, true><<<grid, kThreads, 0, s>>>(a);
-  else fp8_rows_kernel<T, false><<<grid, kThreads, 0, s>>>(a);
+  if (vec) fp8_rows_kernel<T><<<grid, kThreads, 0, s>>>(a);
+  else fp8_rows_any_kernel<T><<<grid, kThreads, 0, s>>>(a);
 }
 
 template <typename T>
