@@ -439,6 +439,8 @@ nvfp4moe_status fp8_gemm(const uint8_t* A, int64_t lda, const float* A_scale, in
  *   xq     = FP8(x), 1 x 128 groups
  *   h      = FP8(silu(xq . Wg[e]^T) * (xq . Wu[e]^T)), 1 x 128 groups of the fp32 products
  *   out[t] = bf16(sum_j w[t][j] * (h . Wd[e]^T)), fp32, in slot order
+ * (Tiles of 128 rows keep the rows h . Wd[e]^T for the combine in fp16 with a power-of-two scale per
+ * row and 128 columns: 2^-11 of a value at most.)
  * x bf16 [T][H], logits fp32 [T][E] (finite), out bf16 [T][H]; all contiguous, x, out and the
  * weights 16-byte aligned, the workspace 256-byte aligned.  H and I: multiples of 16; E <= 1024,
  * 1 <= top_k <= min(E, 32), T * top_k <= 2^24.  Nothing in the workspace is read before the call
@@ -446,11 +448,14 @@ nvfp4moe_status fp8_gemm(const uint8_t* A, int64_t lda, const float* A_scale, in
  * ---------------------------------------------------------------------------- */
 typedef struct {
   int32_t T, H, I, E, top_k;
-  /* NVFP4MOE_LAUNCH_SINGLE: one persistent, cooperative launch (after a small one that zeroes its
-   * counters), for T <= 32 and rows of x that fit in shared memory beside three stages of weights
-   * (H <= 7168 at T <= 16, about half of that above), else NVFP4MOE_UNSUPPORTED_SHAPE;
-   * NVFP4MOE_LAUNCH_MULTI: routing, permutation, quantisation, grouped products and combine as
-   * launches of their own; NVFP4MOE_LAUNCH_AUTO: SINGLE where it fits. */
+  /* NVFP4MOE_LAUNCH_SINGLE: one persistent, cooperative launch (after a small one that quantises x and
+   * zeroes its counters), for T <= 32 and x that fits in shared memory beside three stages of weights
+   * (H up to 6400 at T <= 16 and 2432 above, with 256 experts and top 8), else
+   * NVFP4MOE_UNSUPPORTED_SHAPE;
+   * NVFP4MOE_LAUNCH_MULTI: routing, permutation, quantisation, products and combine as launches of
+   * their own: a stream of weights over groups of 32 rows where experts get few rows each (at most 20 on
+   * average, T <= 256), tiles of 128 rows elsewhere;
+   * NVFP4MOE_LAUNCH_AUTO: SINGLE where it fits. */
   int32_t launch_mode;
   const uint8_t* w13_codes; /* [E][2][I][H]: gate, then up */
   const float* w13_scale;   /* [E][2][ceil(I/128)][ceil(H/128)] */
