@@ -16,6 +16,10 @@
 //                          quantised once and written to its k rows (or, GEMV layout, to the
 //                          token's row); padding rows and the tile map, split over the CTAs.
 // Kernels 2 and 3 are launched as programmatic dependents and wait for their predecessor.
+// The FP8 layer's third kernel quantises x to E4M3 per 128 columns instead (Fp8Place), and its last CTA
+// writes the list of row groups that the expert products run over.
+#include "ffn_gemv.cuh"
+#include "fp8.cuh"
 #include "topk.cuh"
 
 namespace nvfp4moe {
@@ -46,6 +50,7 @@ struct BatchArgs {
   float* zero_rows;         // nullable [T][H] fp32: each slice's rows are zeroed
   int slices;
   int slice;                // tokens per slice
+  Fp8Place fp8;
 };
 
 template <int PER_LANE>
@@ -149,6 +154,88 @@ __global__ void __launch_bounds__(1024) col_scan_kernel(BatchArgs a) {
   }
 }
 
+// The slice's x rows [t0, t0 + nt) in E4M3, four lanes a group of 128, each group quantised once and
+// written to the k rows of its token.
+__device__ __forceinline__ void place_fp8(const BatchArgs& a, int t0, int nt, const int32_t* s_row) {
+  const int nb = (a.H + FP8_BLOCK - 1) / FP8_BLOCK, sub = threadIdx.x & 3;
+  const int groups = nt * nb;
+  for (int g0 = threadIdx.x >> 2; g0 < (groups + 7) / 8 * 8; g0 += kThreads / 4) {  // whole warps
+    const int tl = g0 / nb, b = g0 - tl * nb;
+    uint4 u[4];
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int col = b * FP8_BLOCK + (sub + 4 * j) * 8;
+      u[j] = g0 < groups && col < a.H ? __ldg(reinterpret_cast<const uint4*>(a.x + int64_t(t0 + tl) * a.H + col))
+                                      : make_uint4(0u, 0u, 0u, 0u);
+      m = __vmaxu2(m, __vmaxu2(__vmaxu2(u[j].x & 0x7FFF7FFFu, u[j].y & 0x7FFF7FFFu),
+                               __vmaxu2(u[j].z & 0x7FFF7FFFu, u[j].w & 0x7FFF7FFFu)));
+    }
+    m = max(m << 16, m & 0xFFFF0000u);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    const Fp8ScaleBf16 f = fp8_scale_bf16(m);
+    if (g0 >= groups) continue;
+    uint2 w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t q[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(q[i] << 16);
+        v[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
+      }
+      w[j] = make_uint2(fp8_encode4(v, f), fp8_encode4(v + 4, f));
+    }
+    for (int d = 0; d < a.k; ++d) {
+      const int64_t row = s_row[tl * a.k + d];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int col = b * FP8_BLOCK + (sub + 4 * j) * 8;
+        if (col < a.H) *reinterpret_cast<uint2*>(a.fp8.codes + row * a.H + col) = w[j];
+      }
+      if (sub == 0) a.fp8.scale[row * nb + b] = f.scale;
+    }
+  }
+}
+
+// {expert, first row, rows} for every `group` rows of every expert, [0].x their number, and a zeroed
+// counter for each.
+__device__ __forceinline__ void list_groups(const Fp8Place& p, int E, const int32_t* s_first, const int32_t* s_cnt,
+                                            int32_t* s_sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int first[2], n[2], mine = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int e = 2 * int(threadIdx.x) + i;
+    first[i] = e < E ? s_first[e] : 0;
+    n[i] = e < E ? s_cnt[e] : 0;
+    mine += (n[i] + p.group - 1) / p.group;
+  }
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();  // the scratch was read before
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  int at = incl - mine, total = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) at += s_sum[w];
+    total += s_sum[w];
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    for (int r = 0; r < n[i]; r += p.group)
+      p.groups[1 + at++] = make_int4(2 * int(threadIdx.x) + i, first[i] + r, min(p.group, n[i] - r), 0);
+  if (threadIdx.x == 0) p.groups[0] = make_int4(total, 0, 0, 0);
+  for (int i = threadIdx.x; i < total; i += kThreads) p.counters[i] = 0;
+}
+
+template <bool FP8>
 __global__ void __launch_bounds__(kThreads) place_quant_kernel(BatchArgs a) {
   __shared__ uint32_t s_mask[MAX_E];
   __shared__ int32_t s_start[MAX_E];
@@ -268,6 +355,12 @@ __global__ void __launch_bounds__(kThreads) place_quant_kernel(BatchArgs a) {
   }
   __syncthreads();
 
+  if constexpr (FP8) {
+    place_fp8(a, t0, nt, s_row);
+    if (c == int(gridDim.x) - 1) list_groups(a.fp8, E, s_poff, s_cnt, s_w32);
+    return;  // rows are not padded
+  }
+
   // quantise each 16-element block of the slice's x rows once; write it to its row(s)
   const int nb = H / 16;
   const int64_t rb = H / 2;
@@ -358,13 +451,14 @@ nvfp4moe_status launch_batch_prologue(const void* x, const float* logits, int T,
                                       int32_t* offsets, int32_t* padded_offsets, int32_t* pair_to_row,
                                       int32_t* row_token, int32_t* row_pair, int32_t* tile_expert, int32_t* active,
                                       float* zero_f32, int expert_order, uint8_t* x_codes, uint8_t* x_sf,
-                                      void* scratch, float* zero_rows, void* const* stage_events, cudaStream_t s) {
+                                      void* scratch, float* zero_rows, void* const* stage_events, cudaStream_t s,
+                                      const Fp8Place* fp8) {
   NVFP4_REQUIRE(batch_prologue_fits(T, E, k), NVFP4MOE_UNSUPPORTED_SHAPE, "batch prologue: T=%d E=%d k=%d out of range",
                 T, E, k);
   int lg = 0;
   while ((1 << lg) < m_tile) ++lg;
   NVFP4_REQUIRE((1 << lg) == m_tile, NVFP4MOE_INVALID_ARG, "batch prologue: m_tile %d is not a power of two", m_tile);
-  BatchArgs a;
+  BatchArgs a{};
   a.x = static_cast<const __nv_bfloat16*>(x);
   a.logits = logits;
   a.T = T; a.H = H; a.E = E; a.k = k; a.m_tile_log2 = lg;
@@ -380,6 +474,7 @@ nvfp4moe_status launch_batch_prologue(const void* x, const float* logits, int T,
   a.slices = (T + a.slice - 1) / a.slice;
   a.hist = static_cast<int32_t*>(scratch);
   a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + (int64_t(a.slices) * E * 4 + 255) / 256 * 256);
+  if (fp8) a.fp8 = *fp8;
   auto mark = [&](int i) -> cudaError_t { return stage_events ? record_mark(stage_events[i], s) : cudaSuccess; };
 
   const int per = (E + 31) / 32;
@@ -399,7 +494,9 @@ nvfp4moe_status launch_batch_prologue(const void* x, const float* logits, int T,
   cudaError_t e = mark(1);
   if (e == cudaSuccess) e = launch_dependent(col_scan_kernel, dim3(static_cast<unsigned>((E + 31) / 32)), dim3(1024), 0, s, a);
   if (e == cudaSuccess) e = mark(2);
-  if (e == cudaSuccess) e = launch_dependent(place_quant_kernel, grid, dim3(kThreads), 0, s, a);
+  if (e == cudaSuccess)
+    e = fp8 ? launch_dependent(place_quant_kernel<true>, grid, dim3(kThreads), 0, s, a)
+            : launch_dependent(place_quant_kernel<false>, grid, dim3(kThreads), 0, s, a);
   if (e != cudaSuccess) return fail(NVFP4MOE_CUDA_ERROR, "batch prologue: %s", cudaGetErrorString(e));
   return check_launch("batch prologue");
 }

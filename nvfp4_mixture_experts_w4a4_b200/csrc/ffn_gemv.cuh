@@ -92,6 +92,13 @@ nvfp4moe_status launch_prologue(const void* x, const float* logits, int T, int H
 // Larger-batch prologue (route + permute + quantise x) over 32-token slices in three launches;
 // scratch: batch_prologue_scratch_bytes(T, E) bytes, free until the down GEMM; see
 // batch_prologue.cu.  stage_events (nullable) get marks 1 and 2 after its first two launches.
+struct Fp8Place {  // the FP8 layer: x in E4M3 in expert order, and the row groups of its products
+  uint8_t* codes;    // [pairs][H]
+  float* scale;      // [pairs][ceil(H / 128)]
+  int group;         // rows of a group
+  int4* groups;      // [0].x their number, then {expert, first row, rows, -} each
+  int* counters;     // one for each group, zeroed
+};
 bool batch_prologue_fits(int T, int E, int k);
 int64_t batch_prologue_scratch_bytes(int T, int E);
 nvfp4moe_status launch_batch_prologue(const void* x, const float* logits, int T, int H, int E, int k, int m_tile,
@@ -99,7 +106,8 @@ nvfp4moe_status launch_batch_prologue(const void* x, const float* logits, int T,
                                       int32_t* offsets, int32_t* padded_offsets, int32_t* pair_to_row,
                                       int32_t* row_token, int32_t* row_pair, int32_t* tile_expert, int32_t* active,
                                       float* zero_f32, int expert_order, uint8_t* x_codes, uint8_t* x_sf,
-                                      void* scratch, float* zero_rows, void* const* stage_events, cudaStream_t s);
+                                      void* scratch, float* zero_rows, void* const* stage_events, cudaStream_t s,
+                                      const Fp8Place* fp8 = nullptr);
 // out[t] = bf16(sum_j topk_w[t*k+j] * slots[pair_to_row[t*k+j]]) in slot order, over fp32 slot
 // rows in padded expert order (a programmatic dependent of the down GEMM)
 nvfp4moe_status launch_combine_rows(const float* slots, const int32_t* pair_to_row, const float* topk_w, int T, int H,

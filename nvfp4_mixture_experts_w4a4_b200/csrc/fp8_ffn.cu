@@ -141,7 +141,7 @@ fp8_combine_kernel(const __half* __restrict__ slots, const float* __restrict__ s
 }
 
 struct Layout {
-  int64_t ids, w, counts, offsets, padded, pair_to_row, row_token, row_pair, tile_expert, active, scratch, tiles,
+  int64_t ids, w, counts, offsets, padded, pair_to_row, row_token, row_pair, tile_expert, active, scratch, groups,
       x_codes, x_scale, h_codes, h_scale, slots, slot_scale, counters, parts, total;
   int64_t pairs;
   int group, max_row_tiles;  // rows of a group, groups at most
@@ -209,7 +209,7 @@ Layout make_layout(const fp8_moe_ffn_desc& d) {
   L.pair_to_row = put(P * 4), L.row_token = put(P * 4), L.row_pair = put(P * 4), L.tile_expert = put(P * 4);
   L.active = put((d.E + 1) * 4);
   L.scratch = put(d.T > 0 ? batch_prologue_scratch_bytes(d.T, d.E) : 0);
-  L.tiles = put((int64_t(L.max_row_tiles) + 1) * 16);
+  L.groups = put((int64_t(L.max_row_tiles) + 1) * 16);
   L.counters = put(int64_t(L.max_row_tiles) * 4);
   L.x_codes = put(P * d.H), L.x_scale = put(P * nH * 4);
   L.h_codes = put(P * d.I), L.h_scale = put(P * nI * 4);
@@ -260,31 +260,34 @@ nvfp4moe_status fp8_moe_ffn_forward(const fp8_moe_ffn_desc* desc, const void* x,
     c.x_codes = ws + L.x_codes, c.x_scale = f32(L.x_scale);
     return launch_fp8_layer(c, s);
   }
-  // routing and permutation: one cluster launch for the batches that it takes, else three over slices
-  if (prologue_fits(d.T, d.E, d.top_k))
+  int4* groups = reinterpret_cast<int4*>(ws + L.groups);
+  cudaError_t e = cudaSuccess;
+  if (prologue_fits(d.T, d.E, d.top_k)) {
+    // one cluster launch for routing and permutation, then x
     st = launch_prologue(x, logits, d.T, d.H, d.E, d.top_k, 1, 0, nullptr, i32(L.ids), f32(L.w), i32(L.counts),
                          i32(L.offsets), i32(L.padded), i32(L.pair_to_row), i32(L.row_token), i32(L.row_pair),
                          i32(L.tile_expert), i32(L.active), nullptr, 1, nullptr, nullptr, nullptr, nullptr, 0, 0, s);
-  else
+    if (st != NVFP4MOE_OK) return st;
+    const int64_t x_groups = int64_t(d.T) * fp8_blocks(d.H);
+    e = launch_dependent(fp8_place_kernel, dim3(unsigned(1 + (x_groups * 16 + kPlaceThreads - 1) / kPlaceThreads)),
+                         dim3(kPlaceThreads), 0, s, static_cast<const __nv_bfloat16*>(x),
+                         static_cast<const int32_t*>(i32(L.pair_to_row)), static_cast<const int32_t*>(i32(L.offsets)),
+                         int(d.T), int(d.H), int(d.E), int(d.top_k), ws + L.x_codes, f32(L.x_scale), L.group, groups,
+                         i32(L.counters));
+    NVFP4_REQUIRE(e == cudaSuccess, NVFP4MOE_CUDA_ERROR, "%s: %s", fn, cudaGetErrorString(e));
+  } else {
+    const Fp8Place place{ws + L.x_codes, f32(L.x_scale), L.group, groups, i32(L.counters)};
     st = launch_batch_prologue(x, logits, d.T, d.H, d.E, d.top_k, 1, 0, nullptr, i32(L.ids), f32(L.w), i32(L.counts),
                                i32(L.offsets), i32(L.padded), i32(L.pair_to_row), i32(L.row_token), i32(L.row_pair),
                                i32(L.tile_expert), i32(L.active), nullptr, 1, nullptr, nullptr, ws + L.scratch, nullptr,
-                               nullptr, s);
-  if (st != NVFP4MOE_OK) return st;
-  int4* tiles = reinterpret_cast<int4*>(ws + L.tiles);
-  const int64_t groups = int64_t(d.T) * fp8_blocks(d.H);
-  cudaError_t e = launch_dependent(fp8_place_kernel, dim3(unsigned(1 + (groups * 16 + kPlaceThreads - 1) / kPlaceThreads)),
-                                         dim3(kPlaceThreads), 0, s, static_cast<const __nv_bfloat16*>(x),
-                                         static_cast<const int32_t*>(i32(L.pair_to_row)),
-                                         static_cast<const int32_t*>(i32(L.offsets)), int(d.T), int(d.H), int(d.E),
-                                         int(d.top_k), ws + L.x_codes, f32(L.x_scale), L.group, tiles,
-                                         i32(L.counters));
-  NVFP4_REQUIRE(e == cudaSuccess, NVFP4MOE_CUDA_ERROR, "%s: %s", fn, cudaGetErrorString(e));
+                               nullptr, s, &place);
+    if (st != NVFP4MOE_OK) return st;
+  }
   GroupedArgs g{};
   g.H = d.H, g.I = d.I, g.E = d.E;
   g.rows = L.pairs;
   g.max_row_tiles = L.max_row_tiles;
-  g.tiles = tiles;
+  g.tiles = groups;
   g.x_codes = ws + L.x_codes, g.x_scale = f32(L.x_scale);
   g.w13_codes = d.w13_codes, g.w13_scale = d.w13_scale, g.w2_codes = d.w2_codes, g.w2_scale = d.w2_scale;
   g.h_codes = ws + L.h_codes, g.h_scale = f32(L.h_scale), g.slots = ws + L.slots, g.slot_scale = f32(L.slot_scale);
