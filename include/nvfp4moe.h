@@ -449,9 +449,8 @@ nvfp4moe_status fp8_gemm(const uint8_t* A, int64_t lda, const float* A_scale, in
 typedef struct {
   int32_t T, H, I, E, top_k;
   /* NVFP4MOE_LAUNCH_SINGLE: one persistent, cooperative launch (after a small one that quantises x and
-   * zeroes its counters), for T <= 32 and x that fits in shared memory beside three stages of weights
-   * (H up to 6400 at T <= 16 and 2432 above, with 256 experts and top 8), else
-   * NVFP4MOE_UNSUPPORTED_SHAPE;
+   * zeroes its counters), for T <= 16 and x that fits in shared memory beside three stages of weights
+   * (H up to 6400 with 256 experts and top 8), else NVFP4MOE_UNSUPPORTED_SHAPE;
    * NVFP4MOE_LAUNCH_MULTI: routing, permutation, quantisation, products and combine as launches of
    * their own: a stream of weights over groups of 32 rows where experts get few rows each (at most 20 on
    * average, T <= 256), tiles of 128 rows elsewhere;

@@ -65,7 +65,7 @@ nvfp4moe_status launch_fp8_grouped(const GroupedArgs& g, cudaStream_t s);
 nvfp4moe_status make_fp8_map(CUtensorMap* map, const void* base, int64_t K, int64_t rows, int64_t mats, int64_t pitch,
                              int64_t mat_pitch, int box_rows);
 
-// The whole layer in one persistent launch, for batches of at most 32 tokens (fp8_layer.cu).
+// The whole layer in one persistent launch, for batches of at most 16 tokens (fp8_layer.cu).
 struct Fp8LayerSizes {
   int64_t counters, parts, slots, h_codes, h_scale, x_codes, x_scale;  // elements of their types below
 };

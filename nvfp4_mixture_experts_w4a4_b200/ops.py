@@ -658,26 +658,21 @@ class FP8MoeFFN:
 
     def __init__(self, experts: FP8Experts, top_k: int, launch: int = C.LAUNCH_AUTO):
         """launch: LAUNCH_AUTO, LAUNCH_SINGLE (the whole layer as one persistent launch, batches of
-        at most 32 tokens) or LAUNCH_MULTI."""
+        at most 16 tokens) or LAUNCH_MULTI."""
         self.w = experts
         self.top_k = top_k
         self._ws = {}    # size class (bytes) -> buffer
         self._need = {}  # T -> workspace bytes
         d = C.Fp8MoeFfnDesc()
         d.H, d.I, d.E, d.top_k, d.launch_mode = experts.H, experts.I, experts.E, top_k, launch
-        d.w13_codes, d.w13_scale = experts.w13_codes.data_ptr(), experts.w13_scale.data_ptr()
-        d.w2_codes, d.w2_scale = experts.w2_codes.data_ptr(), experts.w2_scale.data_ptr()
         self._desc = d
-        self._descs = {}  # T -> descriptor
-        self._refs = {}   # T -> (reference to the descriptor, workspace)
+        self._calls = {}  # T -> (descriptor, reference to it, workspace)
 
     def desc(self, T: int) -> C.Fp8MoeFfnDesc:
-        if T not in self._descs:
-            d = C.Fp8MoeFfnDesc()
-            ctypes.pointer(d)[0] = self._desc
-            d.T = T
-            self._descs[T] = d
-        return self._descs[T]
+        d = C.Fp8MoeFfnDesc()
+        ctypes.pointer(d)[0] = self._desc
+        d.T = T
+        return d
 
     def workspace(self, T: int) -> torch.Tensor:
         """The device workspace of a T-token call: pooled by power-of-two size class and never
@@ -707,9 +702,12 @@ class FP8MoeFFN:
         logits = logits.to(torch.float32).contiguous()
         if out is None:
             out = torch.empty((T, w.H), dtype=torch.bfloat16, device=dev)
-        if T not in self._refs:
-            self._refs[T] = (ctypes.byref(self.desc(T)), self.workspace(T))
-        ref, ws = self._refs[T]
+        if T not in self._calls:
+            d = self.desc(T)
+            self._calls[T] = (d, ctypes.byref(d), self.workspace(T))
+        d, ref, ws = self._calls[T]
+        d.w13_codes, d.w13_scale = w.w13_codes.data_ptr(), w.w13_scale.data_ptr()
+        d.w2_codes, d.w2_scale = w.w2_codes.data_ptr(), w.w2_scale.data_ptr()
         _call(dev, "fp8_moe_ffn_forward", ref, x.data_ptr(), logits.data_ptr(), out.data_ptr(), ws.data_ptr(),
               ws.numel())
         return out

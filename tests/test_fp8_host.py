@@ -65,7 +65,7 @@ def desc(**change):
     (dict(I=24), C.UNSUPPORTED_SHAPE), (dict(E=1025), C.UNSUPPORTED_SHAPE), (dict(E=0), C.UNSUPPORTED_SHAPE),
     (dict(top_k=9), C.UNSUPPORTED_SHAPE), (dict(top_k=0), C.UNSUPPORTED_SHAPE),
     (dict(E=64, top_k=33), C.UNSUPPORTED_SHAPE), (dict(T=1 << 24), C.UNSUPPORTED_SHAPE),
-    (dict(launch_mode=7), C.INVALID_ARG), (dict(launch_mode=C.LAUNCH_SINGLE, T=33), C.UNSUPPORTED_SHAPE),
+    (dict(launch_mode=7), C.INVALID_ARG), (dict(launch_mode=C.LAUNCH_SINGLE, T=17), C.UNSUPPORTED_SHAPE),
     (dict(launch_mode=C.LAUNCH_SINGLE, H=16384), C.UNSUPPORTED_SHAPE),
 ])
 def test_layer_statuses(so, change, status):

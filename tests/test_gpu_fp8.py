@@ -256,7 +256,7 @@ def experts(E, I, H, seed):
 def in_tiles(T, E, k, launch=C.LAUNCH_AUTO):
     """Whether a batch runs in row tiles, whose rows of the output wait for the combine in fp16."""
     P = T * k
-    return (T > 32 or launch == C.LAUNCH_MULTI) and (T > 256 or P > 20 * min(P, E))
+    return (T > 16 or launch == C.LAUNCH_MULTI) and (T > 256 or P > 20 * min(P, E))
 
 
 def layer_reference(w, x, logits, k, tiles):
@@ -321,7 +321,7 @@ CASES = [
     # T, H, I, E, k
     (1, 256, 128, 8, 2), (1, 2048, 512, 64, 10), (1, 1024, 4096, 1, 1), (2, 16, 16, 3, 3), (3, 144, 80, 5, 1),
     (8, 256, 128, 8, 2), (15, 1040, 336, 20, 3), (16, 512, 256, 512, 10), (16, 400, 144, 1024, 32), (17, 768, 384, 12, 4),
-    (32, 2048, 128, 40, 8), (32, 256, 128, 1, 1), (33, 256, 128, 8, 2), (45, 1040, 336, 20, 3), (130, 640, 208, 7, 2),
+    (32, 2048, 128, 40, 8), (32, 256, 128, 1, 1), (33, 256, 128, 8, 2), (64, 400, 144, 64, 2), (65, 400, 144, 64, 2), (40, 6144, 144, 4, 4), (45, 1040, 336, 20, 3), (130, 640, 208, 7, 2),
     (300, 384, 512, 3, 1), (600, 272, 128, 300, 5), (16, 7168, 128, 6, 2), (5, 6144, 256, 4, 2), (256, 640, 208, 64, 5),
     (257, 640, 208, 64, 5), (90, 1040, 656, 3, 1), (700, 1552, 96, 5, 2), (1500, 256, 128, 1, 1),
 ]
@@ -341,7 +341,7 @@ def test_layer(T, H, I, E, k):
     assert ops.device_status() == 0
 
 
-@pytest.mark.parametrize("T", [1, 16, 32])
+@pytest.mark.parametrize("T", [1, 7, 16])
 @pytest.mark.parametrize("launch", [C.LAUNCH_SINGLE, C.LAUNCH_MULTI])
 def test_layer_launches(T, launch):
     """Both ways of running a small batch, workspaces reused across changing routings."""
@@ -405,7 +405,7 @@ def test_layer_inputs_and_outputs():
         with pytest.raises(ValueError):
             layer(**bad)
     with pytest.raises(C.Nvfp4MoeError, match="single launch"):
-        ops.FP8MoeFFN(w, 2, launch=C.LAUNCH_SINGLE)(x[:33, :256], logits[:33, :8])
+        ops.FP8MoeFFN(w, 2, launch=C.LAUNCH_SINGLE)(x[:17, :256], logits[:17, :8])
     with pytest.raises(C.Nvfp4MoeError, match="multiple of 16"):
         ops.FP8MoeFFN(experts(2, 24, 256, 1), 1)(x[:4, :256], logits[:4, :2])
 
@@ -493,3 +493,37 @@ def test_a_block_of_a_model(T):
     c, sc = ops.fp8_quantize(z)
     check_gemm(ops.fp8_gemm(c, sc, proj, sp), c, sc, proj, sp)
     assert ops.device_status() == 0
+
+
+def test_two_layers_on_two_streams():
+    """Two layers with workspaces of their own, their launches interleaved on two streams."""
+    g = gen(9)
+    layers = [ops.FP8MoeFFN(experts(12, 256, 512, s), 3) for s in (1, 2)]
+    calls = [[(torch.randn(T, 512, generator=g, device="cuda").bfloat16(), torch.randn(T, 12, generator=g, device="cuda"))
+              for T in (3, 16, 40, 300)] for _ in layers]
+    want = [[layer(*c) for c in cs] for layer, cs in zip(layers, calls)]
+    streams = [torch.cuda.Stream() for _ in layers]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(5):
+        for i in range(4):
+            for n, s in enumerate(streams):
+                with torch.cuda.stream(s):
+                    got[n].append(layers[n](*calls[n][i]))
+    torch.cuda.synchronize()
+    for n in range(2):
+        assert all(torch.equal(y, want[n][i % 4]) for i, y in enumerate(got[n]))
+    assert ops.device_status() == 0
+
+
+def test_weights_can_be_replaced():
+    """A layer reads the experts' tensors as they are at the call."""
+    a, b = experts(4, 128, 256, 1), experts(4, 128, 256, 2)
+    g = gen(3)
+    x, logits = torch.randn(9, 256, generator=g, device="cuda").bfloat16(), torch.randn(9, 4, generator=g, device="cuda")
+    want = ops.FP8MoeFFN(b, 2)(x, logits)
+    layer = ops.FP8MoeFFN(a, 2)
+    assert not torch.equal(layer(x, logits), want)
+    a.w13_codes, a.w13_scale, a.w2_codes, a.w2_scale = b.w13_codes, b.w13_scale, b.w2_codes, b.w2_scale
+    assert torch.equal(layer(x, logits), want)
