@@ -245,6 +245,7 @@ __device__ __forceinline__ void read_columns(uint32_t taddr, uint32_t (&r)[N]) {
 __global__ void __launch_bounds__(256)
 fp8_layer_prepare_kernel(const __nv_bfloat16* __restrict__ x, int T, int H, uint8_t* __restrict__ codes,
                          float* __restrict__ scale, int* __restrict__ counters, int n) {
+  griddep_wait();  // the call before may still use the counters and x
   griddep_launch_dependents();
   for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) counters[i] = 0;
   const int nH = ceil_div(H, 128), sub = threadIdx.x & 7;
@@ -359,6 +360,9 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
   if constexpr (!GROUPED)
     for (int e = threadIdx.x; e < a.E; e += kThreads) s_mask[e] = 0u;
   __syncthreads();
+  // Every CTA is resident and has its TMEM: the next launch may take what is left of the SM and set itself
+  // up.  (Before the allocation it could not: a waiting launch that got the columns first would hold them.)
+  if constexpr (!GROUPED) griddep_launch_dependents();
 
   // ---- routing and the list of touched experts ----
 #pragma unroll
@@ -798,15 +802,17 @@ nvfp4moe_status launch_fp8_layer(const Fp8LayerCall& c, cudaStream_t s) {
   if (st == NVFP4MOE_OK) st = make_fp8_map(&mh, c.h_codes, c.I, int64_t(c.T) * c.k, 1, c.I, c.I, kTokens);
   if (st == NVFP4MOE_OK) st = make_fp8_map(&mx, c.x_codes, c.H, c.T, 1, c.H, c.H, kTokens);
   if (st != NVFP4MOE_OK) return st;
-  fp8_layer_prepare_kernel<<<(c.T * a.nH * 8 + 255) / 256, 256, 0, s>>>(
-      static_cast<const __nv_bfloat16*>(c.x), c.T, c.H, c.x_codes, c.x_scale, c.counters, touched + kMaxParts + 1);
+  cudaError_t e = launch_dependent(fp8_layer_prepare_kernel, dim3((c.T * a.nH * 8 + 255) / 256), dim3(256), 0, s,
+                                   static_cast<const __nv_bfloat16*>(c.x), int(c.T), int(c.H), c.x_codes, c.x_scale,
+                                   c.counters, int(touched + kMaxParts + 1));
+  if (e != cudaSuccess) return fail(NVFP4MOE_CUDA_ERROR, "fp8 layer (prepare): %s", cudaGetErrorString(e));
   const size_t smem = smem_layout(kTokens, a.nH, c.k, c.E, a.stages, false).total;
   const int per = (c.E + 31) / 32, grid = num_sms();
-  const cudaError_t e = per <= 1    ? launch_one<kTokens, 1>(m13, m2, mh, mx, a, grid, smem, s)
-                        : per <= 4  ? launch_one<kTokens, 4>(m13, m2, mh, mx, a, grid, smem, s)
-                        : per <= 8  ? launch_one<kTokens, 8>(m13, m2, mh, mx, a, grid, smem, s)
-                        : per <= 16 ? launch_one<kTokens, 16>(m13, m2, mh, mx, a, grid, smem, s)
-                                    : launch_one<kTokens, 32>(m13, m2, mh, mx, a, grid, smem, s);
+  e = per <= 1    ? launch_one<kTokens, 1>(m13, m2, mh, mx, a, grid, smem, s)
+      : per <= 4  ? launch_one<kTokens, 4>(m13, m2, mh, mx, a, grid, smem, s)
+      : per <= 8  ? launch_one<kTokens, 8>(m13, m2, mh, mx, a, grid, smem, s)
+      : per <= 16 ? launch_one<kTokens, 16>(m13, m2, mh, mx, a, grid, smem, s)
+                  : launch_one<kTokens, 32>(m13, m2, mh, mx, a, grid, smem, s);
   if (e != cudaSuccess) return fail(NVFP4MOE_CUDA_ERROR, "fp8 layer: %s", cudaGetErrorString(e));
   return check_launch("fp8 layer");
 }

@@ -286,9 +286,9 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     if constexpr (MODE == DOWN) prefetch_tensormap(&tmD);
   }
   griddep_wait();  // the operands may come from the launch before
-  griddep_launch_dependents();
   tc_fence_before();
   __syncthreads();
+  griddep_launch_dependents();  // TMEM is taken: a launch that starts now and allocates some cannot keep it from this one
   if constexpr (PAIR) cluster_barrier();  // both CTAs' barriers exist
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
@@ -731,11 +731,10 @@ cudaError_t launch_tiles(const CUtensorMap& a, const CUtensorMap& b, const CUten
     attr[n].val.clusterDim.z = 1;
     ++n;
   }
-  if (MODE != DENSE) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
+  // set-up runs under the end of the launch before, whichever that is; nothing is read or written first
+  attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[n].val.programmaticStreamSerializationAllowed = 1;
+  ++n;
   cfg.attrs = attr;
   cfg.numAttrs = n;
   return cudaLaunchKernelEx(&cfg, kern, a, b, d, p);

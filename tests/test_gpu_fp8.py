@@ -527,3 +527,43 @@ def test_weights_can_be_replaced():
     assert not torch.equal(layer(x, logits), want)
     a.w13_codes, a.w13_scale, a.w2_codes, a.w2_scale = b.w13_codes, b.w13_scale, b.w2_codes, b.w2_scale
     assert torch.equal(layer(x, logits), want)
+
+
+@pytest.mark.parametrize("T", [1, 16, 24, 200])
+def test_calls_that_follow_at_once(T):
+    """Launches set themselves up while the one before still runs: a chain of calls, each on what the
+    last one wrote into buffers that are used again, gives what it gives with a wait after every call."""
+    g = gen(T)
+    H, E, k = 512, 12, 3
+    w = [torch.randn(E, 256, H, generator=g, device="cuda") / math.sqrt(H) for _ in range(2)]
+    w.append(torch.randn(E, H, 256, generator=g, device="cuda") / math.sqrt(256))
+    fp8 = ops.FP8MoeFFN(ops.FP8Experts.from_float(*w), k)
+    fp4 = ops.MoeFFN(ops.NVFP4Experts.from_float(*w), k, None, combine=C.COMBINE_ORDERED)
+    proj, sp = ops.fp8_quantize(torch.randn(H, H, generator=g, device="cuda") / math.sqrt(H), tile=ops.FP8_BLOCKS)
+    router, sr = ops.fp8_quantize(torch.randn(E, H, generator=g, device="cuda") / math.sqrt(H), tile=ops.FP8_BLOCKS)
+    x0 = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    codes, scale = ops.fp8_quantize(x0)
+    x, y, logits = x0.clone(), torch.empty_like(x0), torch.empty(T, E, device="cuda")
+
+    def chain(wait):
+        seen = []
+        x.copy_(x0)
+        wait()
+        for i in range(12):
+            ops.fp8_quantize(x, codes=codes, scale=scale), wait()
+            ops.fp8_gemm(codes, scale, router, sr, out=logits), wait()
+            ops.fp8_gemm(codes, scale, proj, sp, out=y), wait()
+            fp8(y, logits, out=x), wait()
+            fp8(x, logits, out=y), wait()
+            ops.fp8_gemm(codes, scale, proj, sp, out=x), wait()
+            if i % 3 == 2:
+                (fp4(y, logits, out=x), wait(), ops.fp8_gemm(codes, scale, router, sr, out=logits), wait(),
+                 fp8(x, logits, out=y), wait())
+            seen += [x.clone(), y.clone(), logits.clone()]
+        return seen
+
+    want = chain(torch.cuda.synchronize)
+    assert all(bool(torch.isfinite(t).all()) for t in want)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(chain(lambda: None), want))
+    assert ops.device_status() == 0
