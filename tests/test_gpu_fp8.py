@@ -567,3 +567,69 @@ def test_calls_that_follow_at_once(T):
     for _ in range(3):
         assert all(torch.equal(a, b) for a, b in zip(chain(lambda: None), want))
     assert ops.device_status() == 0
+
+
+def fork_and_join(x, proj, sp, fp8, logits, z, seen):
+    """What calls may follow: a copy, a fill, a wait for another stream, a kernel and such a wait at once."""
+    main, side = torch.cuda.current_stream(), torch.cuda.Stream()
+    codes, scale = ops.fp8_quantize(x)
+    y = ops.fp8_gemm(codes, scale, proj, sp)          # after a kernel
+    side.wait_stream(main)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000)
+        a = ops.fp8_gemm(codes, scale, proj, sp)      # after a kernel of another stream, and a delay
+        other = fp8[0](a, logits)
+        z.copy_(other)
+    b = fp8[1](y, logits)                             # while the other stream works
+    main.wait_stream(side)
+    c = fp8[1](z, logits)                             # after a kernel and the other stream's copy
+    z.zero_()
+    z[:1].copy_(c[:1])
+    d = fp8[1](z, logits)                             # after a copy
+    e, se = ops.fp8_quantize(d)
+    side.wait_stream(main)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000)
+        e.zero_()
+    main.wait_stream(side)
+    seen += [y, a, other, b, c, d, ops.fp8_gemm(e, se, proj, sp)]  # after the fill
+    return seen
+
+
+@pytest.mark.parametrize("T", [3, 40, 200])
+def test_what_calls_follow(T):
+    """Eager and captured, calls wait for all that their stream waits for."""
+    g = gen(T)
+    H, E, k = 512, 12, 3
+    w = experts(E, 256, H, 3)
+    proj, sp = ops.fp8_quantize(torch.randn(H, H, generator=g, device="cuda") / math.sqrt(H), tile=ops.FP8_BLOCKS)
+    x, logits = torch.randn(T, H, generator=g, device="cuda").bfloat16(), torch.randn(T, E, generator=g, device="cuda")
+    fp8, z = [ops.FP8MoeFFN(w, k) for _ in range(2)], torch.empty_like(x)
+    # one call at a time, each after a wait
+    want = []
+    y = ops.fp8_gemm(*ops.fp8_quantize(x), proj, sp)
+    torch.cuda.synchronize()
+    b = fp8[0](y, logits)
+    torch.cuda.synchronize()
+    c = fp8[0](b, logits)
+    torch.cuda.synchronize()
+    first = torch.zeros_like(x)
+    first[:1] = c[:1]
+    torch.cuda.synchronize()
+    want = [y, y, b, b, c, fp8[0](first, logits), torch.zeros_like(y)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = fork_and_join(x, proj, sp, fp8, logits, z, [])
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+    graph, static, out = torch.cuda.CUDAGraph(), torch.zeros_like(x), []
+    with torch.cuda.graph(graph):
+        static.copy_(x)
+        fork_and_join(static, proj, sp, fp8, logits, z, out)
+    for _ in range(3):
+        for t in out:
+            t.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out, want))
+    assert ops.device_status() == 0
