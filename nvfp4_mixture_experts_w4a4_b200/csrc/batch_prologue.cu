@@ -57,6 +57,7 @@ template <int PER_LANE>
 __global__ void __launch_bounds__(kThreads) route_hist_kernel(BatchArgs a) {
   __shared__ int32_t s_hist[MAX_E];
   __shared__ float s_red[kWarps];
+  griddep_wait();  // logits, x and the buffers may belong to the launch before
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t0 = blockIdx.x * a.slice;
@@ -479,19 +480,10 @@ nvfp4moe_status launch_batch_prologue(const void* x, const float* logits, int T,
 
   const int per = (E + 31) / 32;
   const dim3 grid(static_cast<unsigned>(a.slices));
-  if (per <= 1)
-    route_hist_kernel<1><<<grid, kThreads, 0, s>>>(a);
-  else if (per <= 4)
-    route_hist_kernel<4><<<grid, kThreads, 0, s>>>(a);
-  else if (per <= 8)
-    route_hist_kernel<8><<<grid, kThreads, 0, s>>>(a);
-  else if (per <= 16)
-    route_hist_kernel<16><<<grid, kThreads, 0, s>>>(a);
-  else
-    route_hist_kernel<32><<<grid, kThreads, 0, s>>>(a);
-  nvfp4moe_status st = check_launch("batch prologue (route)");
-  if (st != NVFP4MOE_OK) return st;
-  cudaError_t e = mark(1);
+  const auto route = per <= 1 ? route_hist_kernel<1> : per <= 4 ? route_hist_kernel<4> : per <= 8 ? route_hist_kernel<8>
+                     : per <= 16 ? route_hist_kernel<16> : route_hist_kernel<32>;
+  cudaError_t e = launch_dependent(route, grid, dim3(kThreads), 0, s, a);
+  if (e == cudaSuccess) e = mark(1);
   if (e == cudaSuccess) e = launch_dependent(col_scan_kernel, dim3(static_cast<unsigned>((E + 31) / 32)), dim3(1024), 0, s, a);
   if (e == cudaSuccess) e = mark(2);
   if (e == cudaSuccess)

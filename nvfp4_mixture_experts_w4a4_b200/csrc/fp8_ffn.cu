@@ -99,6 +99,7 @@ fp8_combine_kernel(const __half* __restrict__ slots, const float* __restrict__ s
   __shared__ int s_row[32];
   __shared__ float s_w[32];
   griddep_wait();
+  griddep_launch_dependents();
   const int64_t t = blockIdx.x;
   if (threadIdx.x < k) {
     s_row[threadIdx.x] = __ldg(pair_to_row + t * k + threadIdx.x);

@@ -117,6 +117,8 @@ constexpr int ctas_of() { return sizeof(T) == 2 ? 2 : 1; }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) fp8_rows_kernel(QuantArgs a) {
+  griddep_wait();  // x may come from the launch before
+  griddep_launch_dependents();
   constexpr int VEC = 16 / sizeof(T);                  // elements of a 16-byte load
   constexpr int kLanes = lanes_of<T>();
   constexpr int CHUNKS = FP8_BLOCK / (VEC * kLanes);   // loads a lane and group: 2 (bf16), 4 (fp32)
@@ -170,6 +172,8 @@ __global__ void __launch_bounds__(kThreads, 4) fp8_rows_kernel(QuantArgs a) {
 // single loads and byte stores are still neighbours'.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) fp8_rows_any_kernel(QuantArgs a) {
+  griddep_wait();  // x may come from the launch before
+  griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int nb = int((a.K + FP8_BLOCK - 1) / FP8_BLOCK);
   const int64_t g = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / 32;
@@ -235,6 +239,10 @@ fp8_blocks_kernel(const __grid_constant__ CUtensorMap tm, QuantArgs a, int64_t b
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1);
     mbar_fence_init();
+  }
+  griddep_wait();  // x may come from the launch before
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
     for (int64_t i = 0; i < STAGES && i < mine; ++i) load(i);
   }
   __syncthreads();
@@ -279,6 +287,8 @@ fp8_blocks_kernel(const __grid_constant__ CUtensorMap tm, QuantArgs a, int64_t b
 // The same for matrices that tile copies do not take: one CTA per block, single loads and stores.
 template <typename T>
 __global__ void __launch_bounds__(kBlockThreads) fp8_blocks_any_kernel(QuantArgs a) {
+  griddep_wait();  // x may come from the launch before
+  griddep_launch_dependents();
   constexpr int WARPS = kBlockThreads / 32, ROWS = FP8_BLOCK / WARPS;
   __shared__ uint32_t s_max[WARPS];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -322,14 +332,14 @@ __global__ void __launch_bounds__(kBlockThreads) fp8_blocks_any_kernel(QuantArgs
 }
 
 template <typename T>
-void launch_rows(const QuantArgs& a, bool vec, cudaStream_t s) {
+nvfp4moe_status launch_rows(const QuantArgs& a, bool vec, cudaStream_t s) {
   // no grid-wide stride: CTAs that finish early make room for the next ones, where a fixed grid's last
   // turn was a third empty at 4096 x 5120
   const int64_t per_block = vec ? depth_of<T>() * kThreads / lanes_of<T>() : kThreads / 32;
   const dim3 grid(static_cast<unsigned>((a.rows * fp8_blocks(a.K) + per_block - 1) / per_block),
                   static_cast<unsigned>(a.batch < 65535 ? a.batch : 65535));
-  if (vec) fp8_rows_kernel<T><<<grid, kThreads, 0, s>>>(a);
-  else fp8_rows_any_kernel<T><<<grid, kThreads, 0, s>>>(a);
+  const cudaError_t e = launch_dependent(vec ? fp8_rows_kernel<T> : fp8_rows_any_kernel<T>, grid, dim3(kThreads), 0, s, a);
+  return e == cudaSuccess ? NVFP4MOE_OK : fail(NVFP4MOE_CUDA_ERROR, "fp8_quantize: %s", cudaGetErrorString(e));
 }
 
 template <typename T>
@@ -338,8 +348,9 @@ nvfp4moe_status launch_blocks(const QuantArgs& a, bool vec, cudaStream_t s) {
   const int64_t pitch = a.rows > 1 ? a.ldx * int64_t(sizeof(T)) : 16;
   const int64_t batch_pitch = a.batch > 1 ? a.x_batch * int64_t(sizeof(T)) : 16;
   if (!vec || pitch >= (int64_t(1) << 40) || batch_pitch >= (int64_t(1) << 40)) {
-    fp8_blocks_any_kernel<T><<<dim3(static_cast<unsigned>(blocks)), kBlockThreads, 0, s>>>(a);
-    return NVFP4MOE_OK;
+    const cudaError_t e = launch_dependent(fp8_blocks_any_kernel<T>, dim3(static_cast<unsigned>(blocks)),
+                                           dim3(kBlockThreads), 0, s, a);
+    return e == cudaSuccess ? NVFP4MOE_OK : fail(NVFP4MOE_CUDA_ERROR, "fp8_quantize: %s", cudaGetErrorString(e));
   }
   uint32_t* status = device_status_ptr();
   auto fn = tensor_map_encoder();
@@ -353,11 +364,12 @@ nvfp4moe_status launch_blocks(const QuantArgs& a, bool vec, cudaStream_t s) {
                         CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(NVFP4MOE_CUDA_ERROR, "fp8_quantize: cuTensorMapEncodeTiled failed (%d)", int(r));
   constexpr int smem = 1024 + kStages * FP8_BLOCK * FP8_BLOCK * int(sizeof(T));
-  const cudaError_t e = set_smem_limit_once<fp8_blocks_kernel<T>>(smem);
-  if (e != cudaSuccess) return fail(NVFP4MOE_CUDA_ERROR, "fp8_quantize: %s", cudaGetErrorString(e));
+  cudaError_t e = set_smem_limit_once<fp8_blocks_kernel<T>>(smem);
   const int64_t most = int64_t(num_sms()) * ctas_of<T>(), grid = blocks < most ? blocks : most;
-  fp8_blocks_kernel<T><<<dim3(static_cast<unsigned>(grid)), kBlockThreads, smem, s>>>(tm, a, blocks, status);
-  return NVFP4MOE_OK;
+  if (e == cudaSuccess)
+    e = launch_dependent(fp8_blocks_kernel<T>, dim3(static_cast<unsigned>(grid)), dim3(kBlockThreads), smem, s, tm, a,
+                         blocks, status);
+  return e == cudaSuccess ? NVFP4MOE_OK : fail(NVFP4MOE_CUDA_ERROR, "fp8_quantize: %s", cudaGetErrorString(e));
 }
 
 }  // namespace
@@ -397,12 +409,9 @@ extern "C" nvfp4moe_status fp8_quantize(const void* x, int32_t x_dtype, int64_t 
   const QuantArgs a{x, batch, rows, K, ldx, x_batch_stride, codes, ldc, codes_batch_stride, scale, lds,
                     scale_batch_stride};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (tile == NVFP4MOE_FP8_ROWS) {
-    if (elt == 2) launch_rows<__nv_bfloat16>(a, vec, s);
-    else launch_rows<float>(a, vec, s);
-  } else {
-    const nvfp4moe_status st = elt == 2 ? launch_blocks<__nv_bfloat16>(a, vec, s) : launch_blocks<float>(a, vec, s);
-    if (st != NVFP4MOE_OK) return st;
-  }
-  return check_launch(fn);
+  const nvfp4moe_status st =
+      tile == NVFP4MOE_FP8_ROWS
+          ? (elt == 2 ? launch_rows<__nv_bfloat16>(a, vec, s) : launch_rows<float>(a, vec, s))
+          : (elt == 2 ? launch_blocks<__nv_bfloat16>(a, vec, s) : launch_blocks<float>(a, vec, s));
+  return st == NVFP4MOE_OK ? check_launch(fn) : st;
 }

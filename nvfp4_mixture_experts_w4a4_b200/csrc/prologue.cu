@@ -88,6 +88,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
   const int gi = c * kThreads + tid;
   constexpr int kAll = kCluster * kThreads;
 
+  griddep_wait();  // logits, x and the buffers may belong to the launch before
   griddep_launch_dependents();  // the grouped GEMM may take the other SMs and set itself up
   // every CTA must have started before any writes into its shared memory
   cluster_arrive_relaxed();
@@ -321,16 +322,10 @@ nvfp4moe_status launch_prologue(const void* x, const float* logits, int T, int H
   a.list = list; a.done = done;
   a.wt_gateup = wt_gateup; a.wt_down = wt_down;
   const int per = (E + 31) / 32;
-  if (per <= 1)
-    prologue_kernel<1><<<kCluster, kThreads, 0, s>>>(a);
-  else if (per <= 4)
-    prologue_kernel<4><<<kCluster, kThreads, 0, s>>>(a);
-  else if (per <= 8)
-    prologue_kernel<8><<<kCluster, kThreads, 0, s>>>(a);
-  else if (per <= 16)
-    prologue_kernel<16><<<kCluster, kThreads, 0, s>>>(a);
-  else
-    prologue_kernel<32><<<kCluster, kThreads, 0, s>>>(a);
+  const auto kern = per <= 1 ? prologue_kernel<1> : per <= 4 ? prologue_kernel<4> : per <= 8 ? prologue_kernel<8>
+                    : per <= 16 ? prologue_kernel<16> : prologue_kernel<32>;
+  const cudaError_t e = launch_dependent(kern, dim3(kCluster), dim3(kThreads), 0, s, a);
+  if (e != cudaSuccess) return fail(NVFP4MOE_CUDA_ERROR, "prologue: %s", cudaGetErrorString(e));
   return check_launch("prologue");
 }
 
