@@ -224,6 +224,18 @@ __device__ __forceinline__ bool wait_count(const int* p, int want) {
   return false;
 }
 __device__ __forceinline__ void add_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// A barrier of the adding warps that tells each whether any of them gave up waiting.  They leave their
+// units together: one that left alone would not come to the next barrier.
+__device__ __forceinline__ bool add_barrier_any(bool gave_up) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 256, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(uint32_t(gave_up))
+      : "memory");
+  return r != 0;
+}
 
 template <int N>
 __device__ __forceinline__ void read_columns(uint32_t taddr, uint32_t (&r)[N]) {
@@ -589,13 +601,13 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
     if (!ok) abort_now();
     griddep_wait();  // the counters are zero
     uint32_t it = 0;
-    for (int i = 0; i < units && ok; ++i) {
+    for (int i = 0; i < units; ++i) {
       const Unit u = unit_of(p, a, i, cta);
       const auto [e, row0, n] = rows_of(u);
       float acc[NT];
 #pragma unroll
       for (int c = 0; c < NT; ++c) acc[c] = 0.0f;
-      for (int j = u.j0; j < u.j1; ++j, ++it) {
+      for (int j = u.j0; j < u.j1 && ok; ++j, ++it) {
         const int slot = it % kSlots;
         if (abort_flag || !mbar_wait(&acc_full[slot], (it / kSlots) & 1)) {
           abort_now();
@@ -625,7 +637,6 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
         __syncwarp();
         if (lane == 0) mbar_arrive(&acc_empty[slot]);
       }
-      if (!ok) break;
       if (u.down) {
         // both halves' sums are one output: the second hands its over
         if (half == 1) {
@@ -633,7 +644,7 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
           for (int c = 0; c < NT; ++c)
             if (c < n) s_buf[c * kPitch + r] = acc[c];
         }
-        add_barrier();
+        if (add_barrier_any(!ok)) break;
         const int col = u.blk * 128 + r;
         if (half == 0 && col < a.H) {
           float* dst = a.slots + (int64_t(row0) * p.s2 + u.part) * a.H + col;
@@ -650,7 +661,7 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
 #pragma unroll
           for (int c = 0; c < NT; ++c)
             if (c < a.T) __stcg(dst + c * 128, acc[c]);
-          add_barrier();
+          if (add_barrier_any(!ok)) break;
           if (threadIdx.x == 128) s_last = add_acq_rel(a.tickets + u.id) == p.s1 - 1;
           add_barrier();
           finish = s_last != 0;
@@ -670,7 +681,7 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
 #pragma unroll
             for (int c = 0; c < NT; ++c) s_buf[c * kPitch + r] = acc[c];
           }
-          add_barrier();
+          if (add_barrier_any(!ok)) break;
           if (half == 0) {
 #pragma unroll
             for (int c = 0; c < NT; ++c)

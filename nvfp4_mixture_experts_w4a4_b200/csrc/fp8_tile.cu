@@ -200,7 +200,18 @@ __device__ __forceinline__ void reg_take() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-__device__ __forceinline__ void add_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// A barrier of the adding warps that tells each whether any of them gave up waiting.  They leave their
+// units together: one that left alone would not come to the next barrier.
+__device__ __forceinline__ bool add_barrier_any(bool gave_up) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, 256, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(uint32_t(gave_up))
+      : "memory");
+  return r != 0;
+}
 
 struct Tile {
   int e;     // matrix of B (expert)
@@ -426,7 +437,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     };
     uint32_t it = 0, batch = 0;
     int done = 0;
-    for (int t = t_first; t < n_tiles && !*abort_flag; t += t_step, ++done) {
+    for (int t = t_first; t < n_tiles && (MODE == GATEUP || !*abort_flag); t += t_step, ++done) {
       const Tile pair_tile = tile_at(t);
       Tile w = pair_tile;  // this CTA's rows of it
       w.row += side * TM;
@@ -494,7 +505,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         __syncwarp();
         if (lane == 0) mbar_arrive(&sc_empty[batch & 1]);
       }
-      if (!ok) break;
+      if (MODE != GATEUP && !ok) break;
 
       if constexpr (SPLIT) {
         // this rank's share, by row, over the idle ring (every stage of it has been consumed)
@@ -526,7 +537,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         }
         uint32_t* sm = s_amax + (done & 1) * 2 * TM;  // two tiles' worth: the barrier below orders reuse
         sm[half * TM + r] = m;
-        add_barrier();
+        if (add_barrier_any(!ok)) break;
         m = max(m, sm[(half ^ 1) * TM + r]);
         const Fp8Scale f = fp8_scale(m);
         if (r < w.rows) {
