@@ -347,7 +347,7 @@ nvfp4moe_status launch_blocks(const QuantArgs& a, bool vec, cudaStream_t s) {
   const int64_t blocks = a.batch * fp8_blocks(a.rows) * fp8_blocks(a.K);
   const int64_t pitch = a.rows > 1 ? a.ldx * int64_t(sizeof(T)) : 16;
   const int64_t batch_pitch = a.batch > 1 ? a.x_batch * int64_t(sizeof(T)) : 16;
-  if (!vec || pitch >= (int64_t(1) << 40) || batch_pitch >= (int64_t(1) << 40)) {
+  if (!vec || pitch >= (int64_t(1) << 40) || batch_pitch >= (int64_t(1) << 40) || batch_pitch == 0) {
     const cudaError_t e = launch_dependent(fp8_blocks_any_kernel<T>, dim3(static_cast<unsigned>(blocks)),
                                            dim3(kBlockThreads), 0, s, a);
     return e == cudaSuccess ? NVFP4MOE_OK : fail(NVFP4MOE_CUDA_ERROR, "fp8_quantize: %s", cudaGetErrorString(e));
@@ -399,6 +399,13 @@ extern "C" nvfp4moe_status fp8_quantize(const void* x, int32_t x_dtype, int64_t 
                 NVFP4MOE_INVALID_ARG, "%s: negative stride", fn);
   NVFP4_REQUIRE(batch * srows <= INT64_MAX / nb && batch * srows * nb <= (int64_t(1) << 31) - 1,
                 NVFP4MOE_UNSUPPORTED_SHAPE, "%s: more than 2^31 - 1 groups", fn);
+  // matrices behind one another, or with their rows interleaved
+  auto apart = [&](int64_t n, int64_t length, int64_t pitch, int64_t stride) {
+    return batch == 1 || stride >= (n - 1) * pitch + length ||
+           (stride >= length && (n == 1 || pitch >= (batch - 1) * stride + length));
+  };
+  NVFP4_REQUIRE(apart(rows, K, ldc, codes_batch_stride) && apart(srows, nb, lds, scale_batch_stride),
+                NVFP4MOE_INVALID_ARG, "%s: the codes or scales of two matrices overlap", fn);
   const int64_t elt = x_dtype == NVFP4MOE_DTYPE_BF16 ? 2 : 4;
   NVFP4_REQUIRE(reinterpret_cast<uintptr_t>(x) % elt == 0, NVFP4MOE_INVALID_ARG, "%s: x is not aligned to its type",
                 fn);

@@ -6,18 +6,32 @@
 // The tensor core sums one 128-element block of K (four tcgen05.mma kind::f8f6f4 of K = 32, fp32
 // accumulators in TMEM); between blocks the partial sum is multiplied by its two scales and added
 // to fp32 registers.  The rows of A are the MMA's M side, so a thread of the adding warps holds one
-// row: both scales are one number a thread, and the multiply-add is one packed FMA for two columns.
-// All of TMEM is accumulators (512 / BN of them), so the MMA of block kb + 1 runs under the
-// additions of block kb.  Per block an SM multiplies for 512 cycles (128 x 256 x 128 at 8192 MACs a
-// cycle) while its eight adding warps read 128 KB of TMEM (256 cycles) and issue 64 packed FMAs a
-// thread (256 cycles a scheduler).
+// row: the product of both scales is one number a thread, and a column costs one FMA.  (The weights
+// on the M side, an expert's rows in steps of 16 on the N side: a third fewer blocks for 256 experts
+// with 128 rows on average, but a scale a column, read from shared memory for every block, and an
+// epilogue across warps; 1300 us a layer of 4096 tokens against 1060.  FMAs packed in pairs: slower,
+// the register pairs cost moves.)  All of TMEM is accumulators (512 / BN of them), so the MMA of block
+// kb + 1 runs under the additions of block kb.  Per block an SM multiplies for 512 cycles (128 x 256 x
+// 128 at 8192 MACs a cycle) while its eight adding warps read 128 KB of TMEM (256 cycles) and issue 256
+// FMAs a scheduler (256 cycles); what a block takes is 1000 to 1200 cycles, for the way between the two
+// (commit, barrier, read, barrier) and for power: 4096 x 5120 x 17408 takes 367 us in a burst (1990 TFLOP/s)
+// and 405 to 440 in a long run, where the clock falls to 1.57 GHz (profiled: the tensor pipe is 41 %
+// active).
 //
 //   warp 0      TMA producer: 128 rows of A and BN rows of B, 128 bytes of K each, per stage
 //   warp 1      TMEM owner and MMA issuer
+//   warps 2, 3  the products of both scales for eight blocks at a time, into shared memory (read by
+//               the adding warps themselves, every eighth block waited out an L2 read: 787 -> 484 us for
+//               4096 x 5120 x 17408)
 //   warps 4..11 additions and epilogue: warp w reads TMEM lanes 32 * (w % 4), the first four take
 //               the left half of the columns and the others the right half
 // A thread that adds holds 128 sums, so the register file is split unevenly: launched with 168
 // registers a thread (384 threads, 64512), warps 0..3 keep 40 and warps 4..11 take 232 (the same sum).
+//
+// Pairs of CTAs (cta_group::2) take 256 x 256 tiles of large dense products: each loads half of B, a
+// third less to load a tile (2048 x 4096 x 4096: 42.6 us, 46.3 unpaired).  Grouped tiles stay single: an
+// expert's rows rarely fill 256.  They run at the weights' rate from memory where experts have few rows
+// (4.6 TB/s at 64 rows an expert), and at the additions' where they have many.
 //
 // Products with few tiles and a long sum split K over the CTAs of a cluster (SPLIT): each adds its
 // share of the blocks, writes its tile to its own shared memory, and the cluster's CTAs sum slices

@@ -615,22 +615,33 @@ class FP8Experts:
     ceil(I / 128)]: one scale per 128 x 128 block, as checkpoints keep them."""
 
     def __init__(self, w13_codes, w13_scale, w2_codes, w2_scale):
-        _fp8_codes(w13_codes, "w13_codes")
-        _fp8_codes(w2_codes, "w2_codes")
         if w13_codes.dim() != 4 or w13_codes.shape[1] != 2:
             raise ValueError(f"w13_codes must be [E, 2, I, H], got {tuple(w13_codes.shape)}")
         self.E, _, self.I, self.H = w13_codes.shape
+        tensors = dict(w13_codes=w13_codes, w13_scale=w13_scale, w2_codes=w2_codes, w2_scale=w2_scale)
+        for name, t in tensors.items():
+            self._check(name, t)
+        for name, t in tensors.items():
+            setattr(self, name, t)
+
+    def _check(self, name, t):
         nI, nH = _fp8_blocks(self.I), _fp8_blocks(self.H)
-        for name, t, shape in (("w2_codes", w2_codes, (self.E, self.H, self.I)),
-                               ("w13_scale", w13_scale, (self.E, 2, nI, nH)),
-                               ("w2_scale", w2_scale, (self.E, nH, nI))):
-            if tuple(t.shape) != shape:
-                raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
-        if w13_scale.dtype != torch.float32 or w2_scale.dtype != torch.float32:
-            raise ValueError("scales must be fp32")
-        _same_device(w13_codes, w13_scale, w2_codes, w2_scale)
-        self.w13_codes, self.w13_scale = w13_codes.contiguous(), w13_scale.contiguous()
-        self.w2_codes, self.w2_scale = w2_codes.contiguous(), w2_scale.contiguous()
+        shape = {"w13_codes": (self.E, 2, self.I, self.H), "w13_scale": (self.E, 2, nI, nH),
+                 "w2_codes": (self.E, self.H, self.I), "w2_scale": (self.E, nH, nI)}[name]
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+        if name.endswith("codes"):
+            _fp8_codes(t, name)
+        elif t.dtype != torch.float32:
+            raise ValueError(f"{name} must be fp32, got {t.dtype}")
+
+    def __setattr__(self, name, value):
+        """The four tensors can be replaced (a layer reads them at the call) by others of their kind."""
+        if name in ("w13_codes", "w13_scale", "w2_codes", "w2_scale"):
+            self._check(name, value)
+            _same_device(value, self.__dict__.get("w13_codes"))
+            value = value.contiguous()
+        super().__setattr__(name, value)
 
     @classmethod
     def from_fp8(cls, gate: tuple, up: tuple, down: tuple) -> "FP8Experts":

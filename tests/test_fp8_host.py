@@ -116,3 +116,13 @@ def test_binding_refuses():
         ops.FP8Experts(w13[:, 0], torch.ones(2, 2, 1, 1), w2, torch.ones(2, 1, 1))
     with pytest.raises(ValueError, match="CUDA"):
         ops.FP8Experts(w13, torch.ones(2, 2, 1, 1), w2, torch.ones(2, 1, 1))
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(), C.INVALID_ARG), (dict(cb=4 * 64 - 1, sb=4), C.INVALID_ARG), (dict(cb=4 * 64, sb=3), C.INVALID_ARG),
+    (dict(cb=4 * 64), C.INVALID_ARG), (dict(sb=4), C.INVALID_ARG), (dict(cb=63, ldc=128, sb=4), C.INVALID_ARG),
+    (dict(cb=64, ldc=127, sb=4), C.INVALID_ARG), (dict(tile=1, cb=4 * 64), C.INVALID_ARG),
+])
+def test_outputs_of_a_batch_stay_apart(so, change, status):
+    assert quantize(so, **{**dict(batch=2, xb=256), **change}) == status
+    assert b"overlap" in so.nvfp4moe_last_error()

@@ -633,3 +633,62 @@ def test_what_calls_follow(T):
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(out, want))
     assert ops.device_status() == 0
+
+
+def test_experts_refuse_other_tensors():
+    w = experts(4, 128, 256, 1)
+    for name, t, match in (("w2_codes", w.w13_codes[:, 0], "w2_codes must be"), ("w2_scale", w.w2_scale.double(), "fp32"),
+                           ("w13_codes", w.w13_codes.float(), "float8"), ("w13_scale", w.w13_scale.cpu(), "CUDA")):
+        with pytest.raises(ValueError, match=match):
+            setattr(w, name, t)
+    wide = torch.zeros(4, 256, 256, dtype=torch.uint8, device="cuda")
+    w.w2_codes = wide[..., :128]
+    assert w.w2_codes.is_contiguous()
+
+
+def test_quantize_matrices_that_share_rows():
+    """One matrix seen as a batch, and codes whose rows lie between those of another matrix."""
+    g = gen(5)
+    x = torch.randn(130, 256, generator=g, device="cuda")
+    for tile in (ops.FP8_ROWS, ops.FP8_BLOCKS):
+        want, scale = ops.fp8_quantize(x, tile=tile)
+        codes, s = ops.fp8_quantize(x.expand(3, 130, 256), tile=tile)
+        assert all(same(c.float(), want.float()) and torch.equal(t, scale) for c, t in zip(codes, s))
+        between = torch.zeros(130, 2, 256, dtype=torch.float8_e4m3fn, device="cuda").transpose(0, 1)
+        ops.fp8_quantize(torch.stack([x, -x]), tile=tile, codes=between)
+        assert same(between[0].float(), want.float()) and same(between[1].float(), (-want.float()))
+        with pytest.raises(RuntimeError, match="overlap"):
+            ops.fp8_quantize(torch.stack([x, x]), tile=tile, codes=want.expand(2, 130, 256))
+
+
+LOWEST = torch.finfo(torch.float32).min
+
+
+@pytest.mark.parametrize("T", [5, 40, 100, 300])
+@pytest.mark.parametrize("mask", [-math.inf, LOWEST])
+def test_layer_masked_experts(T, mask):
+    """Experts masked with -inf or the type's lowest value: all but one, all but k, and (the lowest value)
+    all, which leaves a uniform choice of the first k; a token whose experts are all -inf has no softmax
+    and gives NaN, and the other tokens keep their bits."""
+    E, k = 10, 3
+    w = experts(E, 128, 256, 4)
+    g = gen(T)
+    x, logits = torch.randn(T, 256, generator=g, device="cuda").bfloat16(), torch.randn(T, E, generator=g, device="cuda")
+    layer = ops.FP8MoeFFN(w, k)
+    logits[0, 1:] = mask
+    logits[1, :7] = mask
+    logits[2, 1::2] = mask
+    if mask == LOWEST:
+        logits[3] = mask
+    y = layer(x, logits)
+    check_layer(w, x, logits, k, y)
+    if mask == -math.inf:
+        logits[3] = mask
+        z = layer(x, logits)
+        assert z[3].isnan().all()
+        others = torch.arange(T, device="cuda") != 3
+        if T > 16:  # (moving a token moves rows to other tiles; a row's sums do not depend on that)
+            assert torch.equal(z[others], y[others])
+        else:       # (a single launch splits its sums by the number of experts that are touched)
+            check_layer(w, x[others], logits[others], k, z[others])
+    assert ops.device_status() == 0
