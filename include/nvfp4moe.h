@@ -413,7 +413,8 @@ nvfp4moe_status moe_ffn_forward(const moe_ffn_desc* desc, const void* x, const f
  * stride in elements), codes [batch][rows][K] (pitch ldc, bytes), scale (pitch lds, elements).
  * tile: NVFP4MOE_FP8_ROWS (1 x 128) or NVFP4MOE_FP8_BLOCKS (128 x 128).  Any sizes and pitches;
  * 16-byte aligned rows of x and 8-byte aligned rows of codes are read and written widest.  Bytes
- * of codes between K and the pitch are left as they are.
+ * of codes between K and the pitch are left as they are.  The matrices of a batch may share x
+ * (x_batch_stride 0) but not codes or scales: each behind the other, or with their rows interleaved.
  *
  * fp8_gemm - D[M][N] = A . B^T: A [M][K] with 1 x 128 scales, B [N][K] with 128 x 128 scales, D
  * bf16 or fp32 (d_dtype).  Products of one 128-block of K are summed in fp32 by the tensor cores,
