@@ -13,10 +13,12 @@
 // the register pairs cost moves.)  All of TMEM is accumulators (512 / BN of them), so the MMA of block
 // kb + 1 runs under the additions of block kb.  Per block an SM multiplies for 512 cycles (128 x 256 x
 // 128 at 8192 MACs a cycle) while its eight adding warps read 128 KB of TMEM (256 cycles) and issue 256
-// FMAs a scheduler (256 cycles); what a block takes is 1000 to 1200 cycles, for the way between the two
-// (commit, barrier, read, barrier) and for power: 4096 x 5120 x 17408 takes 367 us in a burst (1990 TFLOP/s)
-// and 405 to 440 in a long run, where the clock falls to 1.57 GHz (profiled: the tensor pipe is 41 %
-// active).
+// FMAs a scheduler (256 cycles).  What a block takes is 1000 to 1200 cycles.  Dense: 4096 x 5120 x 17408 in
+// pairs 391 us, 306 with the additions left out; the rest is the way between the MMA and the additions
+// (commit, barrier, read, barrier), and in a long run power (405 to 440 us at 1.57 GHz, 367 in a burst:
+// 1990 TFLOP/s).  Grouped, with experts of 128 rows and more: the loads, 10 TB/s from L2 of which 4.5 come
+// from memory (4096 tokens, 256 experts of 4096 x 1024: the layer 993 us, 928 with the additions left out,
+// the same with three stages as with four, and 6 to 14 % more with prefetches into L2).
 //
 //   warp 0      TMA producer: 128 rows of A and BN rows of B, 128 bytes of K each, per stage
 //   warp 1      TMEM owner and MMA issuer
@@ -29,9 +31,10 @@
 // registers a thread (384 threads, 64512), warps 0..3 keep 40 and warps 4..11 take 232 (the same sum).
 //
 // Pairs of CTAs (cta_group::2) take 256 x 256 tiles of large dense products: each loads half of B, a
-// third less to load a tile (2048 x 4096 x 4096: 42.6 us, 46.3 unpaired).  Grouped tiles stay single: an
-// expert's rows rarely fill 256.  They run at the weights' rate from memory where experts have few rows
-// (4.6 TB/s at 64 rows an expert), and at the additions' where they have many.
+// third less to load (2048 x 4096 x 4096: 42.6 us, 46.3 unpaired).  Grouped tiles stay single: an
+// expert's rows rarely fill 256 (gate/up 588 us in pairs, 490 single, 256 experts with 128 rows on
+// average).  Where experts have few rows the weights' rate from memory bounds them (4.5 TB/s, which a
+// stream of 250 MB reaches with nothing else to do).
 //
 // Products with few tiles and a long sum split K over the CTAs of a cluster (SPLIT): each adds its
 // share of the blocks, writes its tile to its own shared memory, and the cluster's CTAs sum slices
