@@ -501,7 +501,7 @@ def _same_device(*ts):
 
 def _call(dev, fn: str, *args):
     """Calls the library with `dev` current and its current stream as the last argument."""
-    now = torch.cuda.current_device()
+    now = torch._C._cuda_getDevice()  # (torch.cuda.current_device without its check for initialisation)
     if now == dev.index:
         st = getattr(lib(), fn)(*args, torch._C._cuda_getCurrentRawStream(now))
     else:
@@ -511,8 +511,17 @@ def _call(dev, fn: str, *args):
         check(st, fn)
 
 
+def _empty(shape, dtype, dev):
+    """torch.empty; with the strides given it takes 1.5 us of the host's time instead of 2.4."""
+    strides = (shape[1], 1) if len(shape) == 2 else (shape[1] * shape[2], shape[2], 1)
+    return torch.empty_strided(shape, strides, dtype=dtype, device=dev)
+
+
+_E4M3, _U8, _F32 = torch.float8_e4m3fn, torch.uint8, torch.float32
+
+
 def _fp8_codes(t: torch.Tensor, what: str):
-    if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+    if t.dtype is not _E4M3 and t.dtype is not _U8:
         raise ValueError(f"{what} must be float8_e4m3fn (or its bytes as uint8), got {t.dtype}")
 
 
@@ -542,9 +551,10 @@ def fp8_quantize(x: torch.Tensor, *, tile: int = FP8_ROWS, codes: torch.Tensor |
         raise ValueError("x must have unit stride along K")
     nk = (K + 127) // 128
     srows = rows if tile == FP8_ROWS else (rows + 127) // 128
+    batch = shape[:-2]
     if codes is None:
         pitch = (K + 15) // 16 * 16
-        codes = torch.empty((*shape[:-1], pitch), dtype=torch.float8_e4m3fn, device=dev)
+        codes = _empty((*batch, rows, pitch), torch.float8_e4m3fn, dev)
         if pitch != K:
             codes = codes[..., :K]
     else:
@@ -552,12 +562,12 @@ def fp8_quantize(x: torch.Tensor, *, tile: int = FP8_ROWS, codes: torch.Tensor |
         if codes.shape != shape or (K > 1 and codes.stride(-1) != 1):
             raise ValueError(f"codes must be {tuple(shape)} with unit stride along K")
     if scale is None:
-        scale = torch.empty((*shape[:-2], srows, nk), dtype=torch.float32, device=dev)
-    elif (scale.dtype != torch.float32 or scale.shape != (*shape[:-2], srows, nk)
+        scale = _empty((*batch, srows, nk), torch.float32, dev)
+    elif (scale.dtype != torch.float32 or scale.shape != (*batch, srows, nk)
           or (nk > 1 and scale.stride(-1) != 1)):
-        raise ValueError(f"scale must be fp32 {(*shape[:-2], srows, nk)} with unit stride along K")
+        raise ValueError(f"scale must be fp32 {(*batch, srows, nk)} with unit stride along K")
     cs, ss = codes.stride(), scale.stride()
-    if x.dim() == 3:
+    if batch:
         B, xb, cb, sb = shape[0], stride[0], cs[0], ss[0]
     else:
         B, xb, cb, sb = 1, 0, 0, 0
@@ -578,20 +588,20 @@ def fp8_gemm(A: torch.Tensor, A_scale: torch.Tensor, B: torch.Tensor, B_scale: t
         raise ValueError(f"A must be [M, K] and B [N, K], got {tuple(A.shape)} and {tuple(B.shape)}")
     M, K = A.shape
     N = B.shape[0]
-    nk = _fp8_blocks(K)
-    if A_scale.dtype != torch.float32 or A_scale.shape != (M, nk):
+    nk = (K + 127) // 128
+    if A_scale.dtype is not _F32 or A_scale.shape != (M, nk):
         raise ValueError(f"A_scale must be fp32 {(M, nk)}, got {A_scale.dtype} {tuple(A_scale.shape)}")
-    if B_scale.dtype != torch.float32 or B_scale.shape != (_fp8_blocks(N), nk):
+    if B_scale.dtype is not _F32 or B_scale.shape != ((N + 127) // 128, nk):
         raise ValueError(f"B_scale must be fp32 {(_fp8_blocks(N), nk)}, got {B_scale.dtype} {tuple(B_scale.shape)}")
     if out is not None:
         out_dtype = out.dtype
         if out.shape != (M, N):
             raise ValueError(f"out must be {(M, N)}, got {tuple(out.shape)}")
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    if out_dtype is not torch.bfloat16 and out_dtype is not _F32:
         raise ValueError("D is bf16 or fp32")
     dev = _same_device(A, A_scale, B, B_scale, out)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        out = _empty((M, N), out_dtype, dev)
     (lda, ka), (ldb, kb), (lds_a, na), (lds_b, nb), (ldd, no) = (
         A.stride(), B.stride(), A_scale.stride(), B_scale.stride(), out.stride())
     if (K > 1 and (ka != 1 or kb != 1)) or (N > 1 and no != 1) or (nk > 1 and (na != 1 or nb != 1)):
@@ -605,7 +615,7 @@ def fp8_gemm(A: torch.Tensor, A_scale: torch.Tensor, B: torch.Tensor, B_scale: t
     if N <= 128:
         lds_b = nk
     _call(dev, "fp8_gemm", A.data_ptr(), lda, A_scale.data_ptr(), lds_a, B.data_ptr(), ldb, B_scale.data_ptr(), lds_b,
-          M, N, K, out.data_ptr(), ldd, C.DTYPE_F32 if out_dtype == torch.float32 else C.DTYPE_BF16)
+          M, N, K, out.data_ptr(), ldd, C.DTYPE_F32 if out_dtype is _F32 else C.DTYPE_BF16)
     return out
 
 
@@ -712,7 +722,7 @@ class FP8MoeFFN:
         x = x.contiguous()
         logits = logits.to(torch.float32).contiguous()
         if out is None:
-            out = torch.empty((T, w.H), dtype=torch.bfloat16, device=dev)
+            out = _empty((T, w.H), torch.bfloat16, dev)
         if T not in self._calls:
             d = self.desc(T)
             self._calls[T] = (d, ctypes.byref(d), self.workspace(T))
