@@ -1,6 +1,7 @@
 // fp8_moe_ffn_forward: the routed feed-forward layer on FP8 weights with a scale per 128 x 128
-// block.  Routing and permutation are the NVFP4 layer's (one order for both), x is quantised per
-// row and 128 columns into expert order, and the products run in fp8_tile.cu.
+// block.  Batches of at most 16 tokens are one launch (fp8_layer.cu).  Otherwise routing and permutation
+// are the NVFP4 layer's (one order for both), x is quantised per row and 128 columns into expert order,
+// and the products run as a stream of weights (fp8_layer.cu) or in tiles of rows (fp8_tile.cu).
 #include <cuda_fp16.h>
 
 #include "ffn_gemv.cuh"
