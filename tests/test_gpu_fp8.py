@@ -692,3 +692,18 @@ def test_layer_masked_experts(T, mask):
         else:       # (a single launch splits its sums by the number of experts that are touched)
             check_layer(w, x[others], logits[others], k, z[others])
     assert ops.device_status() == 0
+
+
+def test_layer_rows_past_32_bits():
+    """560,000 rows of 4096: rows, codes and scales past 2^31 elements.  A row's sums do not depend on the
+    batch, so the last tokens get what a small batch of them gets."""
+    T, H, E, k = 70_000, 4096, 16, 8
+    g = gen(1)
+    w = experts(E, 128, H, 1)
+    x = torch.randn(T, H, generator=g, device="cuda", dtype=torch.bfloat16)
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    layer = ops.FP8MoeFFN(w, k)
+    y = layer(x, logits)
+    for part in (slice(0, 300), slice(T // 2, T // 2 + 300), slice(T - 300, T)):
+        assert torch.equal(y[part], ops.FP8MoeFFN(w, k)(x[part], logits[part]))
+    assert ops.device_status() == 0
