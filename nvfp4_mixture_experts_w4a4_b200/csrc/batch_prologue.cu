@@ -15,7 +15,7 @@
 //                          moe_permute; then each 16-element block of the slice's x rows is
 //                          quantised once and written to its k rows (or, GEMV layout, to the
 //                          token's row); padding rows and the tile map, split over the CTAs.
-// Kernels 2 and 3 are launched as programmatic dependents and wait for their predecessor.
+// All three are launched as programmatic dependents and wait for their predecessor.
 // The FP8 layer's third kernel quantises x to E4M3 per 128 columns instead (Fp8Place), and its last CTA
 // writes the list of row groups that the expert products run over.
 #include "ffn_gemv.cuh"
