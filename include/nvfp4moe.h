@@ -440,8 +440,6 @@ nvfp4moe_status fp8_gemm(const uint8_t* A, int64_t lda, const float* A_scale, in
  *   xq     = FP8(x), 1 x 128 groups
  *   h      = FP8(silu(xq . Wg[e]^T) * (xq . Wu[e]^T)), 1 x 128 groups of the fp32 products
  *   out[t] = bf16(sum_j w[t][j] * (h . Wd[e]^T)), fp32, in slot order
- * (Tiles of 128 rows keep the rows h . Wd[e]^T for the combine in fp16 with a power-of-two scale per
- * row and 128 columns: 2^-11 of a value at most.)
  * x bf16 [T][H], logits fp32 [T][E] (finite), out bf16 [T][H]; all contiguous, x, out and the
  * weights 16-byte aligned, the workspace 256-byte aligned.  H and I: multiples of 16; E <= 1024,
  * 1 <= top_k <= min(E, 32), T * top_k <= 2^24.  Nothing in the workspace is read before the call

@@ -2,8 +2,6 @@
 // block.  Batches of at most 16 tokens are one launch (fp8_layer.cu).  Otherwise routing and permutation
 // are the NVFP4 layer's (one order for both), x is quantised per row and 128 columns into expert order,
 // and the products run as a stream of weights (fp8_layer.cu) or in tiles of rows (fp8_tile.cu).
-#include <cuda_fp16.h>
-
 #include "ffn_gemv.cuh"
 #include "fp8.cuh"
 #include "fp8_tile.cuh"
@@ -89,62 +87,9 @@ fp8_place_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict_
   }
 }
 
-// out[t] = bf16(sum_j w[t][j] * row), fp32, in slot order, over fp16 rows in expert order with a scale per
-// row and 128 columns.  A CTA takes 2048 columns of a token, a thread eight; eight slots are read before
-// the first is added.
-constexpr int kCombineColumns = 8 * 256;
-__global__ void __launch_bounds__(256)
-fp8_combine_kernel(const __half* __restrict__ slots, const float* __restrict__ slot_scale,
-                   const int32_t* __restrict__ pair_to_row, const float* __restrict__ w, int H, int k,
-                   __nv_bfloat16* __restrict__ out) {
-  __shared__ int s_row[32];
-  __shared__ float s_w[32];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int64_t t = blockIdx.x;
-  if (threadIdx.x < k) {
-    s_row[threadIdx.x] = __ldg(pair_to_row + t * k + threadIdx.x);
-    s_w[threadIdx.x] = __ldg(w + t * k + threadIdx.x);
-  }
-  __syncthreads();
-  const int n = blockIdx.y * kCombineColumns + threadIdx.x * 8;
-  if (n >= H) return;
-  const int nb = (H + FP8_BLOCK - 1) / FP8_BLOCK, b = n / FP8_BLOCK;
-  float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int j0 = 0; j0 < k; j0 += 8) {
-    uint4 v[8];
-    float f[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (j0 + u < k) {
-        const int64_t row = s_row[j0 + u];
-        v[u] = __ldcs(reinterpret_cast<const uint4*>(slots + row * H + n));
-        f[u] = s_w[j0 + u] * __ldg(slot_scale + row * nb + b);
-      }
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (j0 + u < k) {
-        const uint32_t q[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&q[c]));
-          acc[2 * c] = fmaf(f[u], y.x, acc[2 * c]);
-          acc[2 * c + 1] = fmaf(f[u], y.y, acc[2 * c + 1]);
-        }
-      }
-  }
-  uint32_t o[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    const __nv_bfloat162 y = __floats2bfloat162_rn(acc[2 * c], acc[2 * c + 1]);
-    o[c] = *reinterpret_cast<const uint32_t*>(&y);
-  }
-  *reinterpret_cast<uint4*>(out + t * H + n) = make_uint4(o[0], o[1], o[2], o[3]);
-}
-
 struct Layout {
   int64_t ids, w, counts, offsets, padded, pair_to_row, row_token, row_pair, tile_expert, active, scratch, groups,
-      x_codes, x_scale, h_codes, h_scale, slots, slot_scale, counters, parts, total;
+      x_codes, x_scale, h_codes, h_scale, slots, counters, parts, total;
   int64_t pairs;
   int group, max_row_tiles;  // rows of a group, groups at most
   bool single, stream;
@@ -215,8 +160,7 @@ Layout make_layout(const fp8_moe_ffn_desc& d) {
   L.counters = put(int64_t(L.max_row_tiles) * 4);
   L.x_codes = put(P * d.H), L.x_scale = put(P * nH * 4);
   L.h_codes = put(P * d.I), L.h_scale = put(P * nI * 4);
-  L.slots = put(P * d.H * (L.stream ? 4 : 2));
-  L.slot_scale = L.stream ? 0 : put(P * nH * 4);
+  L.slots = put(P * d.H * 4);
   L.total = at;
   return L;
 }
@@ -263,7 +207,6 @@ nvfp4moe_status fp8_moe_ffn_forward(const fp8_moe_ffn_desc* desc, const void* x,
     return launch_fp8_layer(c, s);
   }
   int4* groups = reinterpret_cast<int4*>(ws + L.groups);
-  cudaError_t e = cudaSuccess;
   if (prologue_fits(d.T, d.E, d.top_k)) {
     // one cluster launch for routing and permutation, then x
     st = launch_prologue(x, logits, d.T, d.H, d.E, d.top_k, 1, 0, nullptr, i32(L.ids), f32(L.w), i32(L.counts),
@@ -271,7 +214,7 @@ nvfp4moe_status fp8_moe_ffn_forward(const fp8_moe_ffn_desc* desc, const void* x,
                          i32(L.tile_expert), i32(L.active), nullptr, 1, nullptr, nullptr, nullptr, nullptr, 0, 0, s);
     if (st != NVFP4MOE_OK) return st;
     const int64_t x_groups = int64_t(d.T) * fp8_blocks(d.H);
-    e = launch_dependent(fp8_place_kernel, dim3(unsigned(1 + (x_groups * 16 + kPlaceThreads - 1) / kPlaceThreads)),
+    const cudaError_t e = launch_dependent(fp8_place_kernel, dim3(unsigned(1 + (x_groups * 16 + kPlaceThreads - 1) / kPlaceThreads)),
                          dim3(kPlaceThreads), 0, s, static_cast<const __nv_bfloat16*>(x),
                          static_cast<const int32_t*>(i32(L.pair_to_row)), static_cast<const int32_t*>(i32(L.offsets)),
                          int(d.T), int(d.H), int(d.E), int(d.top_k), ws + L.x_codes, f32(L.x_scale), L.group, groups,
@@ -292,20 +235,10 @@ nvfp4moe_status fp8_moe_ffn_forward(const fp8_moe_ffn_desc* desc, const void* x,
   g.tiles = groups;
   g.x_codes = ws + L.x_codes, g.x_scale = f32(L.x_scale);
   g.w13_codes = d.w13_codes, g.w13_scale = d.w13_scale, g.w2_codes = d.w2_codes, g.w2_scale = d.w2_scale;
-  g.h_codes = ws + L.h_codes, g.h_scale = f32(L.h_scale), g.slots = ws + L.slots, g.slot_scale = f32(L.slot_scale);
-  if (L.stream) {
-    st = launch_fp8_stream(g, i32(L.counters), s);
-    if (st != NVFP4MOE_OK) return st;
-    return launch_combine_rows(f32(L.slots), i32(L.pair_to_row), f32(L.w), d.T, d.H, d.top_k, out, s);
-  }
-  st = launch_fp8_grouped(g, s);
+  g.h_codes = ws + L.h_codes, g.h_scale = f32(L.h_scale), g.slots = f32(L.slots);
+  st = L.stream ? launch_fp8_stream(g, i32(L.counters), s) : launch_fp8_grouped(g, s);
   if (st != NVFP4MOE_OK) return st;
-  e = launch_dependent(fp8_combine_kernel, dim3(unsigned(d.T), unsigned((d.H + kCombineColumns - 1) / kCombineColumns)),
-                       dim3(256), 0, s, reinterpret_cast<const __half*>(ws + L.slots),
-                       static_cast<const float*>(f32(L.slot_scale)), static_cast<const int32_t*>(i32(L.pair_to_row)),
-                       static_cast<const float*>(f32(L.w)), int(d.H), int(d.top_k), static_cast<__nv_bfloat16*>(out));
-  NVFP4_REQUIRE(e == cudaSuccess, NVFP4MOE_CUDA_ERROR, "%s: combine: %s", fn, cudaGetErrorString(e));
-  return check_launch(fn);
+  return launch_combine_rows(f32(L.slots), i32(L.pair_to_row), f32(L.w), d.T, d.H, d.top_k, out, s);
 }
 
 }  // extern "C"

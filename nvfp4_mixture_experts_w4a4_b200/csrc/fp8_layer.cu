@@ -838,7 +838,7 @@ nvfp4moe_status launch_fp8_stream(const GroupedArgs& g, int* counters, cudaStrea
   for (a.stages = kMaxStages; smem_layout(nt, 0, 0, 0, a.stages, true).total > kSmemLimit; --a.stages) {
   }
   a.w13_scale = g.w13_scale, a.w2_scale = g.w2_scale;
-  a.h_codes = g.h_codes, a.h_scale = g.h_scale, a.slots = static_cast<float*>(g.slots);
+  a.h_codes = g.h_codes, a.h_scale = g.h_scale, a.slots = g.slots;
   a.done = counters;
   a.status = device_status_ptr();
   if (!a.status) return fail(NVFP4MOE_CUDA_ERROR, "device status word unavailable");

@@ -68,13 +68,14 @@ constexpr int SC_FLOATS = SC_BLOCKS * 2 * TM;   // [block][half][row]
 // rows of B a CTA holds per stage, stages, and shared memory
 constexpr int b_rows(int bn, bool pair) { return pair ? bn / 2 : bn; }
 constexpr int stages_of(int mode, int bn, bool pair) { return mode == DOWN ? 3 : (b_rows(bn, pair) == 256 ? 4 : 6); }
-constexpr int OUT_BLOCK = 32 * 128;  // down: 32 rows x 64 columns of fp16, one a warp, on their way out
+constexpr int OUT_BLOCK = 32 * 128;  // down: 32 rows x 32 columns of fp32, two a warp, on their way out
 constexpr int ring_bytes(int mode, int bn, bool pair) {
-  return stages_of(mode, bn, pair) * (A_STAGE + b_rows(bn, pair) * TK) + (mode == DOWN ? ADD_WARPS * OUT_BLOCK : 0);
+  return stages_of(mode, bn, pair) * (A_STAGE + b_rows(bn, pair) * TK) + (mode == DOWN ? 2 * ADD_WARPS * OUT_BLOCK : 0);
 }
+constexpr int amax_bytes(int mode) { return mode == GATEUP ? 2 * 2 * TM * 4 : 0; }
 constexpr int smem_bytes(int mode, int bn, bool pair) {
   return 1024 + ring_bytes(mode, bn, pair) + (2 * stages_of(mode, bn, pair) + 2 * (512 / bn) + 5) * 8 + 16 +
-         2 * 2 * TM * 4 + 2 * SC_FLOATS * 4;
+         amax_bytes(mode) + 2 * SC_FLOATS * 4;
 }
 constexpr int split_pitch(int bn) { return bn + 4; }  // floats; rows 16 bytes apart in the banks
 
@@ -195,12 +196,6 @@ __device__ __forceinline__ void store_32b(void* p, const uint32_t (&r)[8]) {
                : "memory");
 }
 
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -286,8 +281,8 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   uint64_t* drain = sc_empty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  uint32_t* s_amax = reinterpret_cast<uint32_t*>(tmem_holder + 4);  // [2][2][128]: tile parity, half, row
-  float* s_scale = reinterpret_cast<float*>(s_amax + 4 * TM);       // [2][SC_BLOCKS][2][128]
+  uint32_t* s_amax = reinterpret_cast<uint32_t*>(tmem_holder + 4);  // gate/up: [2][2][128]: tile parity, half, row
+  float* s_scale = reinterpret_cast<float*>(s_amax + amax_bytes(MODE) / 4);  // [2][SC_BLOCKS][2][128]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -574,47 +569,39 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
           }
         }
       } else if constexpr (MODE == DOWN) {
-        // The row's 128 columns in fp16, times a power of two that brings the largest to [2^14, 2^15):
-        // half the bytes of fp32 rows, twice (written here, read by the combine), for 2^-11 of a
-        // value, an eighth of the output's own rounding to bf16.
         const int n = w.n0 + half * HALF;
         if (live && n < p.N) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int i = 0; i < HALF; ++i) m = max(m, abs_bits(acc[i]));
-          // (no scaling for zero, infinite and NaN rows; 2^126 at most)
-          const int up = m == 0u || m >= 0x7F800000u ? 0 : min(126, 141 - int(m >> 23));
-          const float f = __uint_as_float(uint32_t(127 + up) << 23);
-          if (r < w.rows) p.d_scale[int64_t(w.row + r) * p.ldd_s + n / TK] = __uint_as_float(uint32_t(127 - up) << 23);
-          uint8_t* out = smem + STAGES * (A_STAGE + B_STAGE) + (warp - 4) * OUT_BLOCK;
+          uint8_t* out = smem + STAGES * (A_STAGE + B_STAGE) + (warp - 4) * 2 * OUT_BLOCK;
           const bool whole = q * 32 + 32 <= w.rows;  // the rows after the last are another tile's
 #pragma unroll
-          for (int c = 0; c < HALF; c += 64) {
-            uint4 o[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float* v = acc + c + 8 * i;
-              o[i] = make_uint4(f16x2(v[0] * f, v[1] * f), f16x2(v[2] * f, v[3] * f), f16x2(v[4] * f, v[5] * f),
-                                f16x2(v[6] * f, v[7] * f));
-            }
+          for (int c = 0; c < HALF; c += 32) {
             if (whole) {
               // through shared memory and a tile store: 128 bytes of a row at a time (a lane storing its
-              // own row takes a turn for every 32 bytes: 7000 cycles a tile in fp32)
-              bulk_wait_group_read<0>();
+              // own row takes a turn for every 32 bytes: 7000 cycles a tile)
+              uint8_t* block = out + (c / 32 & 1) * OUT_BLOCK;
+              bulk_wait_group_read<1>();
               __syncwarp();
 #pragma unroll
-              for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(out + lane * 128 + ((i ^ (lane & 7)) << 4)) = o[i];
+              for (int i = 0; i < 8; ++i) {
+                const float* v = acc + c + 4 * i;
+                *reinterpret_cast<float4*>(block + lane * 128 + ((i ^ (lane & 7)) << 4)) = make_float4(v[0], v[1], v[2], v[3]);
+              }
               fence_proxy_async_shared();
               __syncwarp();
-              if (lane == 0 && n + c < p.N) {
-                tma_store_2d(&tmD, n + c, w.row + q * 32, out);
+              if (lane == 0) {
+                if (n + c < p.N) tma_store_2d(&tmD, n + c, w.row + q * 32, block);
                 bulk_commit_group();
               }
             } else if (r < w.rows) {
-              uint16_t* d = static_cast<uint16_t*>(p.D) + int64_t(w.row + r) * p.ldd + n + c;
+              float* d = static_cast<float*>(p.D) + int64_t(w.row + r) * p.ldd + n + c;
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (n + c + 8 * i < p.N) *reinterpret_cast<uint4*>(d + 8 * i) = o[i];  // N is a multiple of 16
+              for (int i = 0; i < 32; i += 8)
+                if (n + c + i < p.N) {  // N is a multiple of 16
+                  uint32_t o[8];
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(acc[c + i + j]);
+                  store_32b(d + i, o);
+                }
             }
           }
         }
@@ -825,18 +812,18 @@ int resident_clusters(int split) {
 
 namespace {
 
-// fp16 [rows][H], box 64 columns x 32 rows, 128-byte swizzle; stores past the last column are clipped.
-nvfp4moe_status make_f16_rows_map(CUtensorMap* map, void* base, int64_t rows, int64_t H) {
+// fp32 [rows][H], box 32 columns x 32 rows, 128-byte swizzle; stores past the last column are clipped.
+nvfp4moe_status make_f32_rows_map(CUtensorMap* map, void* base, int64_t rows, int64_t H) {
   auto fn = tensor_map_encoder();
   if (!fn) return fail(NVFP4MOE_CUDA_ERROR, "cuTensorMapEncodeTiled is unavailable");
   const cuuint64_t dims[2] = {cuuint64_t(H), cuuint64_t(rows)};
-  const cuuint64_t strides[1] = {cuuint64_t(H * 2)};
-  const cuuint32_t box[2] = {64u, 32u};
+  const cuuint64_t strides[1] = {cuuint64_t(H * 4)};
+  const cuuint32_t box[2] = {32u, 32u};
   const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims, strides, box, estr,
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return fail(NVFP4MOE_CUDA_ERROR, "cuTensorMapEncodeTiled (fp16 rows) failed (%d)", int(r));
+  if (r != CUDA_SUCCESS) return fail(NVFP4MOE_CUDA_ERROR, "cuTensorMapEncodeTiled (fp32 rows) failed (%d)", int(r));
   return NVFP4MOE_OK;
 }
 
@@ -919,8 +906,7 @@ nvfp4moe_status launch_fp8_grouped(const GroupedArgs& g, cudaStream_t s) {
     st = make_fp8_map(&w13, g.w13_codes, g.H, g.I, 2 * int64_t(g.E), g.H, int64_t(g.I) * g.H, TM);
   if (st == NVFP4MOE_OK) st = make_fp8_map(&hm, g.h_codes, g.I, g.rows, 1, g.I, g.I, 32);
   if (st == NVFP4MOE_OK) st = make_fp8_map(&w2, g.w2_codes, g.I, g.H, g.E, g.I, int64_t(g.I) * g.H, 256);
-  if (st != NVFP4MOE_OK) return st;
-  if (st == NVFP4MOE_OK) st = make_f16_rows_map(&dm, g.slots, g.rows, g.H);
+  if (st == NVFP4MOE_OK) st = make_f32_rows_map(&dm, g.slots, g.rows, g.H);
   if (st != NVFP4MOE_OK) return st;
   TileParams p{};
   p.a_box = 32;
@@ -936,11 +922,11 @@ nvfp4moe_status launch_fp8_grouped(const GroupedArgs& g, cudaStream_t s) {
   const int64_t most = int64_t(g.max_row_tiles) * nI;
   const int grid1 = int(most < num_sms() ? most : num_sms());
   cudaError_t e = launch_tiles<GATEUP, 256, false, false>(xm, w13, w13, p, grid1, s);
-  // down: fp16 rows and their scales in expert order
+  // down: fp32 rows in expert order
   p.nkb = nI, p.n_nt = int((g.H + 255) / 256), p.nsb = nH, p.N = g.H;
   p.sa = g.h_scale, p.lda_s = nI;
   p.sb = g.w2_scale, p.ldb_s = nI, p.sb_e = int64_t(nH) * nI;
-  p.D = g.slots, p.ldd = g.H, p.d_scale = g.slot_scale, p.ldd_s = nH;
+  p.D = g.slots, p.ldd = g.H;
   const int64_t most2 = int64_t(g.max_row_tiles) * p.n_nt;
   const int grid2 = int(most2 < num_sms() ? most2 : num_sms());
   if (e == cudaSuccess) e = launch_tiles<DOWN, 256, false, false>(hm, w2, dm, p, grid2, s);

@@ -21,8 +21,6 @@ struct TileParams {
   void* D;
   int64_t ldd;
   int d_f32, d_vec;
-  float* d_scale;            // down: D is fp16, its value times d_scale[row * ldd_s + column / 128]
-  int64_t ldd_s;
   uint8_t* h_codes;          // gate/up: h in E4M3, rows of A
   float* h_scale;
   int64_t ldh, ldh_s;
@@ -55,8 +53,7 @@ struct GroupedArgs {
   const float* w2_scale;     // [E][H / 128][I / 128]
   uint8_t* h_codes;          // [rows][I]
   float* h_scale;            // [rows][I / 128]
-  void* slots;               // [rows][H]: fp32 (launch_fp8_stream), or fp16 with slot_scale (launch_fp8_grouped)
-  float* slot_scale;         // [rows][H / 128]
+  float* slots;              // [rows][H]
 };
 nvfp4moe_status launch_fp8_grouped(const GroupedArgs& g, cudaStream_t s);
 

@@ -707,3 +707,47 @@ def test_layer_rows_past_32_bits():
     for part in (slice(0, 300), slice(T // 2, T // 2 + 300), slice(T - 300, T)):
         assert torch.equal(y[part], ops.FP8MoeFFN(w, k)(x[part], logits[part]))
     assert ops.device_status() == 0
+
+
+def twins(E, I, H, seed):
+    """Experts 2e and 2e + 1 that differ by the factor -(1 + 2^-9) of their down weights alone."""
+    w = experts(E, I, H, seed)
+    twice = lambda t: t.repeat_interleave(2, 0)  # noqa: E731
+    s2 = twice(w.w2_scale)
+    s2[1::2] *= -(1 + 2.0 ** -9)
+    return w, ops.FP8Experts(twice(w.w13_codes.view(torch.uint8)), twice(w.w13_scale),
+                             twice(w.w2_codes.view(torch.uint8)), s2)
+
+
+@pytest.mark.parametrize("T", [5, 100, 300])
+def test_layer_rows_that_cancel(T):
+    """A token whose two experts' rows nearly cancel: out = -2^-9 y / 2, where y is the layer of one of the
+    twins alone (read in bf16: half a step, 2^-9 of y; the output's own: the same).  The rows' fp32 sums, one
+    block of I, lose at most 2^-24 each in the two scales' product, the scaling, the weighting and the sum: four of
+    2^-24 for each of two rows, over 2^-9: 2^-12 of the output."""
+    H, I = 256, 128
+    one, two = twins(1, I, H, 5)
+    x = torch.randn(T, H, generator=gen(T), device="cuda").bfloat16()
+    y = ops.FP8MoeFFN(one, 1)(x, torch.zeros(T, 1, device="cuda")).double()
+    got = ops.FP8MoeFFN(two, 2)(x, torch.zeros(T, 2, device="cuda")).double()
+    want = -y * 2.0 ** -10
+    assert ((got - want).abs() <= want.abs() * (2 * BF16_HALF + 2.0 ** -12) * (1 + BF16_HALF)).all()
+
+
+@pytest.mark.parametrize("T", [5, 100, 300])
+@pytest.mark.parametrize("e", [-40, 0, 40])
+def test_layer_columns_stay_apart(T, e):
+    """A NaN code in one row of the down weights makes one column of the output NaN, and no other bit
+    changes, whatever the size of its neighbours."""
+    H, I = 256, 128
+    w = experts(1, I, H, 6)
+    x, logits = torch.randn(T, H, generator=gen(T), device="cuda").bfloat16(), torch.zeros(T, 1, device="cuda")
+    w.w2_scale = w.w2_scale * 2.0 ** e
+    clean = ops.FP8MoeFFN(w, 1)(x, logits)
+    codes = w.w2_codes.view(torch.uint8).clone()
+    codes[0, 5, 3], codes[0, 200, 7] = 0x7F, 0xFF
+    got = ops.FP8MoeFFN(ops.FP8Experts(w.w13_codes, w.w13_scale, codes, w.w2_scale), 1)(x, logits)
+    hit = torch.zeros(H, dtype=torch.bool, device="cuda")
+    hit[[5, 200]] = True
+    assert got[:, hit].isnan().all()
+    assert torch.equal(got[:, ~hit], clean[:, ~hit])
