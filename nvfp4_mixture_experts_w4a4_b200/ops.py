@@ -646,7 +646,10 @@ class FP8Experts:
             raise ValueError(f"{name} must be fp32, got {t.dtype}")
 
     def __setattr__(self, name, value):
-        """The four tensors can be replaced (a layer reads them at the call) by others of their kind."""
+        """The four tensors can be replaced (a layer reads them at the call) by others of their kind; the
+        sizes are the tensors'."""
+        if name in ("E", "I", "H") and name in self.__dict__:
+            raise AttributeError(f"{name} is the size of the experts' tensors")
         if name in ("w13_codes", "w13_scale", "w2_codes", "w2_scale"):
             self._check(name, value)
             _same_device(value, self.__dict__.get("w13_codes"))
@@ -680,19 +683,25 @@ class FP8MoeFFN:
     def __init__(self, experts: FP8Experts, top_k: int, launch: int = C.LAUNCH_AUTO):
         """launch: LAUNCH_AUTO, LAUNCH_SINGLE (the whole layer as one persistent launch, batches of
         at most 16 tokens) or LAUNCH_MULTI."""
+        self._ws = {}     # (device, size class in bytes) -> buffer
+        self._need = {}   # T -> workspace bytes
+        self._calls = {}  # T -> (descriptor, reference to it, workspace)
         self.w = experts
         self.top_k = top_k
-        self._ws = {}    # size class (bytes) -> buffer
-        self._need = {}  # T -> workspace bytes
-        d = C.Fp8MoeFfnDesc()
-        d.H, d.I, d.E, d.top_k, d.launch_mode = experts.H, experts.I, experts.E, top_k, launch
-        self._desc = d
-        self._calls = {}  # T -> (descriptor, reference to it, workspace)
+        self.launch = launch
+
+    def __setattr__(self, name, value):
+        """The experts, top_k and the launch can be replaced: what was worked out for them goes with them."""
+        if name == "w" and not isinstance(value, FP8Experts):
+            raise ValueError(f"experts must be FP8Experts, got {type(value).__name__}")
+        super().__setattr__(name, value)
+        if name in ("w", "top_k", "launch"):
+            self._need.clear()
+            self._calls.clear()
 
     def desc(self, T: int) -> C.Fp8MoeFfnDesc:
-        d = C.Fp8MoeFfnDesc()
-        ctypes.pointer(d)[0] = self._desc
-        d.T = T
+        d, w = C.Fp8MoeFfnDesc(), self.w
+        d.T, d.H, d.I, d.E, d.top_k, d.launch_mode = T, w.H, w.I, w.E, self.top_k, self.launch
         return d
 
     def workspace(self, T: int) -> torch.Tensor:
@@ -703,10 +712,10 @@ class FP8MoeFFN:
             if need == 0 and T > 0:
                 check(C.UNSUPPORTED_SHAPE, "fp8_moe_ffn_workspace_size")
             self._need[T] = max(need, 16)
-        size_class = max(1 << 20, 1 << (self._need[T] - 1).bit_length())
-        if size_class not in self._ws:
-            self._ws[size_class] = torch.empty(size_class, dtype=torch.uint8, device=self.w.w13_codes.device)
-        return self._ws[size_class]
+        key = self.w.w13_codes.device, max(1 << 20, 1 << (self._need[T] - 1).bit_length())
+        if key not in self._ws:
+            self._ws[key] = torch.empty(key[1], dtype=torch.uint8, device=key[0])
+        return self._ws[key]
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
         w = self.w

@@ -126,3 +126,46 @@ def test_binding_refuses():
 def test_outputs_of_a_batch_stay_apart(so, change, status):
     assert quantize(so, **{**dict(batch=2, xb=256), **change}) == status
     assert b"overlap" in so.nvfp4moe_last_error()
+
+
+def stand_in(E, I, H):
+    """Experts whose tensors are on the CPU (the class takes CUDA tensors alone)."""
+    w, nI, nH = ops.FP8Experts.__new__(ops.FP8Experts), -(-I // 128), -(-H // 128)
+    w.__dict__.update(E=E, I=I, H=H, w13_codes=torch.zeros(E, 2, I, H, dtype=torch.uint8),
+                      w13_scale=torch.ones(E, 2, nI, nH), w2_codes=torch.zeros(E, H, I, dtype=torch.uint8),
+                      w2_scale=torch.ones(E, nH, nI))
+    return w
+
+
+def test_layer_calls_follow_their_experts(so, monkeypatch):
+    """A layer whose experts, top_k or launch are replaced calls the library with the sizes and workspace of the
+    new ones (the calls are recorded here, not made)."""
+    calls = []
+    monkeypatch.setattr(ops, "_same_device", lambda *ts: torch.device("cpu"))
+    monkeypatch.setattr(ops, "_call", lambda dev, fn, ref, x, lg, out, ws, n: calls.append((ref._obj, ws, n)))
+
+    def call(layer, T):
+        layer(torch.zeros(T, layer.w.H, dtype=torch.bfloat16), torch.zeros(T, layer.w.E))
+        d, ws, n = calls[-1]
+        return {f: getattr(d, f) for f, _ in d._fields_}, n
+
+    first, second = stand_in(64, 256, 256), stand_in(8, 128, 528)
+    layer = ops.FP8MoeFFN(first, 8)
+    for T in (4, 40):
+        assert call(layer, T)[0]["E"] == 64
+    layer.w, layer.top_k = second, 2
+    for T in (4, 40):
+        d, n = call(layer, T)
+        want, m = call(ops.FP8MoeFFN(second, 2), T)
+        assert d == want and d["E"] == 8 and d["I"] == 128 and d["H"] == 528 and d["top_k"] == 2
+        assert n >= so.fp8_moe_ffn_workspace_size(ctypes.byref(layer.desc(T)))
+        assert d["w13_codes"] == second.w13_codes.data_ptr() and d["w2_scale"] == second.w2_scale.data_ptr()
+    layer.launch = C.LAUNCH_MULTI
+    assert call(layer, 4)[0]["launch_mode"] == C.LAUNCH_MULTI
+    layer.top_k = 9
+    with pytest.raises(C.Nvfp4MoeError, match="top_k"):
+        call(layer, 4)
+    with pytest.raises(ValueError, match="FP8Experts"):
+        layer.w = object()
+    with pytest.raises(AttributeError, match="size"):
+        second.E = 64

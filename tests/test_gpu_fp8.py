@@ -751,3 +751,19 @@ def test_layer_columns_stay_apart(T, e):
     hit[[5, 200]] = True
     assert got[:, hit].isnan().all()
     assert torch.equal(got[:, ~hit], clean[:, ~hit])
+
+
+@pytest.mark.parametrize("T", [4, 40, 300])
+def test_layers_take_other_experts(T):
+    """Other experts, of other sizes, and another top_k on a layer that has run: the bits of a layer made with
+    them, before and after."""
+    first, second = experts(64, 256, 256, 1), experts(8, 128, 528, 2)
+    g = gen(T)
+    xs = [torch.randn(T, w.H, generator=g, device="cuda").bfloat16() for w in (first, second)]
+    ls = [torch.randn(T, w.E, generator=g, device="cuda") for w in (first, second)]
+    layer = ops.FP8MoeFFN(first, 8)
+    for w, k, x, l in ((first, 8, xs[0], ls[0]), (second, 2, xs[1], ls[1]), (second, 3, xs[1], ls[1]),
+                       (first, 1, xs[0], ls[0]), (first, 8, xs[0], ls[0])):
+        layer.w, layer.top_k = w, k
+        assert torch.equal(layer(x, l), ops.FP8MoeFFN(w, k)(x, l))
+    assert ops.device_status() == 0
