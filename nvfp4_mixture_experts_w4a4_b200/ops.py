@@ -757,7 +757,10 @@ class GraphedMoeFFN:
     to a pinned host buffer (`out_host`), so one replay is the whole host-to-host step.  Fill
     the host inputs in place (or pass host tensors, which are first copied into them on the
     CPU); the returned `out_host` is valid once the current stream has reached the replay's
-    end (e.g. after torch.cuda.current_stream().synchronize())."""
+    end (e.g. after torch.cuda.current_stream().synchronize()).
+
+    The graph reads the weights where they were at the capture and keeps them alive.  Values written
+    into them are seen; a call after the layer's weights or settings were replaced raises RuntimeError."""
 
     def __init__(self, layer: MoeFFN | FP8MoeFFN, T: int, host_io: bool = False):
         dev = layer.w.w13_codes.device
@@ -782,8 +785,14 @@ class GraphedMoeFFN:
             layer(self.x, self.logits, out=self.out)
             if host_io:
                 self.out_host.copy_(self.out, non_blocking=True)
+        # the layer's and its experts' tensors and settings (a name with an underscore is a cache)
+        self._held = [(vars(o), n, v) for o in (layer, layer.w) for n, v in vars(o).items() if n[0] != "_"]
 
     def __call__(self, x: torch.Tensor = None, logits: torch.Tensor = None) -> torch.Tensor:
+        for owner, name, value in self._held:
+            now = owner.get(name)
+            if now is not value and not (isinstance(value, int) and now == value):
+                raise RuntimeError(f"the layer's {name} was replaced since the capture: capture it again")
         if self.host_io:
             for src, dst in ((x, self.x_host), (logits, self.logits_host)):
                 if src is not None and src.data_ptr() != dst.data_ptr():

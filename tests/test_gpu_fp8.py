@@ -7,6 +7,7 @@ products is taken to lose at most 2^-22 of S per addition (twice an fp32 half-st
 cost 2^-24 each and the additions over the blocks nkb 2^-24, so |error| <= (4 * 128 + nkb + 2) 2^-24 S, plus
 half a step of the output type, finfo(t).eps / 2 of the value.  The layer: see layer_reference."""
 import math
+import weakref
 
 import pytest
 import torch
@@ -767,3 +768,50 @@ def test_layers_take_other_experts(T):
         layer.w, layer.top_k = w, k
         assert torch.equal(layer(x, l), ops.FP8MoeFFN(w, k)(x, l))
     assert ops.device_status() == 0
+
+
+@pytest.mark.parametrize("T", [4, 40])
+def test_graphs_refuse_replaced_weights(T):
+    """A captured call holds the tensors that it reads, follows values written into them, and refuses to run
+    once the layer has others; a new capture takes those.  The NVFP4 layer's graphs do the same."""
+    a, b = experts(8, 128, 256, 1), experts(8, 128, 256, 2)
+    g = gen(T)
+    x, logits = torch.randn(T, 256, generator=g, device="cuda").bfloat16(), torch.randn(T, 8, generator=g, device="cuda")
+    want = [ops.FP8MoeFFN(w, 2)(x, logits) for w in (a, b)]
+    layer = ops.FP8MoeFFN(a, 2)
+    graph = ops.GraphedMoeFFN(layer, T)
+    assert torch.equal(graph(x, logits), want[0])
+    old = [(n, getattr(a, n)) for n in ("w13_codes", "w13_scale", "w2_codes", "w2_scale")]
+    refs = [weakref.ref(t) for _, t in old]
+    for n, t in old:
+        setattr(a, n, getattr(b, n))
+        with pytest.raises(RuntimeError, match=n):
+            graph(x, logits)
+        setattr(a, n, t)
+    assert torch.equal(graph(x, logits), want[0])
+    for n, _ in old:
+        setattr(a, n, getattr(b, n))
+    del old, t
+    assert all(r() is not None for r in refs)
+    assert torch.equal(ops.GraphedMoeFFN(layer, T)(x, logits), want[1])
+    for n, r in zip(("w13_codes", "w13_scale", "w2_codes", "w2_scale"), refs):
+        setattr(a, n, r())
+    assert torch.equal(graph(x, logits), want[0])
+    for name, value in (("w", b), ("top_k", 3), ("launch", C.LAUNCH_MULTI)):
+        was = getattr(layer, name)
+        setattr(layer, name, value)
+        with pytest.raises(RuntimeError, match=name):
+            graph(x, logits)
+        setattr(layer, name, was)
+    for n in ("w13_codes", "w2_codes"):
+        getattr(a, n).view(torch.uint8).copy_(getattr(b, n).view(torch.uint8))
+    a.w13_scale.copy_(b.w13_scale), a.w2_scale.copy_(b.w2_scale)
+    assert torch.equal(graph(x, logits), want[1])
+
+    ws = [torch.randn(4, n, k, generator=g, device="cuda") for n, k in ((128, 256), (128, 256), (256, 128))]
+    fp4 = ops.MoeFFN(ops.NVFP4Experts.from_float(*ws), 2, None)
+    graph, want = ops.GraphedMoeFFN(fp4, T), fp4(x, logits[:, :4])
+    assert torch.equal(graph(x, logits[:, :4]), want)
+    fp4.w.w2_sf = fp4.w.w2_sf.clone()
+    with pytest.raises(RuntimeError, match="w2_sf"):
+        graph(x, logits[:, :4])
