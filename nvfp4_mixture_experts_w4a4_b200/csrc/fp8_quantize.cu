@@ -206,7 +206,8 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_any_kernel(QuantArgs a) {
 
 // 128 x 128 blocks, one after another in a persistent CTA: tile copies bring the next blocks to shared memory
 // (192 KB in flight) while the threads hold the current one in registers, find its maximum and write
-// its codes.  Warp w holds rows w, w + 16, ...; a lane four consecutive columns.  (Blocks loaded to
+// its codes.  Warp w holds rows w, w + 16, ...; a lane four consecutive columns.  Waits are bounded: a CTA that
+// gives up issues no more copies and leaves once those in flight have landed.  (Blocks loaded to
 // registers by a CTA each, two CTAs an SM, waited at their barriers with nothing in flight: 4.5 TB/s at
 // 17400 x 5004 fp32.)
 template <typename T>
@@ -249,7 +250,6 @@ fp8_blocks_kernel(const __grid_constant__ CUtensorMap tm, QuantArgs a, int64_t b
   for (int64_t i = 0; i < mine; ++i) {
     const int s = int(i % STAGES);
     const bool ok = mbar_wait(&full[s], uint32_t(i / STAGES) & 1);
-    if (!ok && lane == 0) atomicOr(status, uint32_t(NVFP4MOE_DEV_TIMEOUT));
     uint32_t u[ROWS][W], m = 0;
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
@@ -265,10 +265,17 @@ fp8_blocks_kernel(const __grid_constant__ CUtensorMap tm, QuantArgs a, int64_t b
     }
     m = __reduce_max_sync(0xffffffffu, m);
     if (lane == 0) s_max[i & 1][warp] = m;
-    __syncthreads();  // the block is in registers, and every warp's maximum is here
+    // the block is in registers, and every warp's maximum is here; where a thread gave up waiting, all leave
+    if (__syncthreads_or(!ok)) {
+      if (threadIdx.x == 0) {
+        atomicOr(status, uint32_t(NVFP4MOE_DEV_TIMEOUT));
+        for (int64_t j = i; j < i + STAGES && j < mine; ++j)  // the copies land before the CTA leaves
+          mbar_wait(&full[j % STAGES], uint32_t(j / STAGES) & 1, 1u << 16);
+      }
+      return;
+    }
     if (threadIdx.x == 0 && i + STAGES < mine) load(i + STAGES);
     const auto f = scale_for<T>(__reduce_max_sync(0xffffffffu, s_max[i & 1][lane % WARPS]));
-    if (!ok) continue;
     int64_t bi, rb, b;
     place(i, bi, rb, b);
     if (threadIdx.x == 0) a.scale[bi * a.s_batch + rb * a.lds + b] = f.scale;
