@@ -215,10 +215,17 @@ __device__ __forceinline__ int add_acq_rel(int* p) {
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
-// Waits until *p >= want; false when it gave up.
+// Waits until *p >= want; false when it gave up.  The second form is a whole warp's, which gets one answer.
 __device__ __forceinline__ bool wait_count(const int* p, int want) {
   for (uint32_t i = 0; i < kPolls; ++i) {
     if (load_acquire(p) >= want) return true;
+    __nanosleep(32);
+  }
+  return false;
+}
+__device__ __forceinline__ bool wait_count_warp(const int* p, int want) {
+  for (uint32_t i = 0; i < kPolls; ++i) {
+    if (__all_sync(0xffffffffu, load_acquire(p) >= want)) return true;
     __nanosleep(32);
   }
   return false;
@@ -443,6 +450,7 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
     abort_flag = 1;
     atomicOr(a.status, kTimeout);
   };
+  auto warp_aborted = [&]() { return __any_sync(0xffffffffu, abort_flag) != 0; };  // one answer for a whole warp
   // the expert of a unit, its first row in expert order and its rows
   struct Rows {
     int e, row0, n;
@@ -537,7 +545,7 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
     int have = -1;  // the expert whose h is known to be complete
     bool ok = true;
     griddep_wait();  // the counters are zero
-    for (int i = 0; i < units && ok && !abort_flag; ++i) {
+    for (int i = 0; i < units && ok && !warp_aborted(); ++i) {
       const Unit u = unit_of(p, a, i, cta);
       const auto [e, row0, n] = rows_of(u);
       for (int j = u.j0; j < u.j1; ++j, ++it) {
@@ -547,7 +555,7 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
         if (u.down) {
           if (lane < 2 && 2 * j + lane < a.nI) sb = __ldg(a.w2_scale + (int64_t(e) * a.nH + u.blk) * a.nI + 2 * j + lane);
           if (u.a != have) {
-            if (!wait_count(a.done + u.a, a.nI)) {
+            if (!wait_count_warp(a.done + u.a, a.nI)) {
               abort_now();
               ok = false;
               break;
@@ -558,7 +566,8 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
         } else if (lane < 2) {
           sb = __ldg(a.w13_scale + ((int64_t(e) * 2 + lane) * a.nI + u.blk) * a.nH + j);
         }
-        if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1) || !mbar_wait(&acc_empty[slot], ((it / kSlots) & 1) ^ 1)) {
+        if (!mbar_wait_warp(&empty[s], ((it / S) & 1) ^ 1) ||
+            !mbar_wait_warp(&acc_empty[slot], ((it / kSlots) & 1) ^ 1)) {
           abort_now();
           ok = false;
           break;
@@ -597,7 +606,7 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
   } else if (warp >= 4 && warp < 12) {
     const int half = (warp - 4) >> 2, q = warp & 3, r = q * 32 + lane;
     const uint32_t trow = tmem + (uint32_t(q * 32) << 16);
-    bool ok = GROUPED || mbar_wait(x_full, 0);
+    bool ok = GROUPED || mbar_wait_warp(x_full, 0);
     if (!ok) abort_now();
     griddep_wait();  // the counters are zero
     uint32_t it = 0;
@@ -609,7 +618,7 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
       for (int c = 0; c < NT; ++c) acc[c] = 0.0f;
       for (int j = u.j0; j < u.j1 && ok; ++j, ++it) {
         const int slot = it % kSlots;
-        if (abort_flag || !mbar_wait(&acc_full[slot], (it / kSlots) & 1)) {
+        if (warp_aborted() || !mbar_wait_warp(&acc_full[slot], (it / kSlots) & 1)) {
           abort_now();
           ok = false;
           break;

@@ -319,6 +319,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     *abort_flag = 1;
     atomicOr(p.status, kTimeout);
   };
+  auto warp_aborted = [&]() { return __any_sync(0xffffffffu, *abort_flag) != 0; };  // one answer for a whole warp
 
   const int ranks = SPLIT ? p.split : 1;
   const int rank = SPLIT ? int(blockIdx.x) % ranks : 0;
@@ -399,7 +400,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       const int l = (warp - 2) * 32 + lane;
       uint32_t batch = 0;
       Tile next = tile_at(t_first);
-      for (int t = t_first; t < n_tiles && !*abort_flag; t += t_step) {
+      for (int t = t_first; t < n_tiles && !warp_aborted(); t += t_step) {
         const Tile w = next;
         next = tile_at(t + t_step);
         const float* sa[2];
@@ -419,7 +420,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
             for (int i = 0; i < 2; ++i) a[i][j] = __ldg(sa[i] + min(kb + j, last));
           const float b = __ldg(sb + min(kb + (lane & 7), last));
-          if (!mbar_wait(&sc_empty[batch & 1], ((batch >> 1) & 1) ^ 1)) {
+          if (!mbar_wait_warp(&sc_empty[batch & 1], ((batch >> 1) & 1) ^ 1)) {
             abort_now();
             break;
           }
@@ -449,7 +450,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     };
     uint32_t it = 0, batch = 0;
     int done = 0;
-    for (int t = t_first; t < n_tiles && (MODE == GATEUP || !*abort_flag); t += t_step, ++done) {
+    for (int t = t_first; t < n_tiles && (MODE == GATEUP || !warp_aborted()); t += t_step, ++done) {
       const Tile pair_tile = tile_at(t);
       Tile w = pair_tile;  // this CTA's rows of it
       w.row += side * TM;
@@ -462,7 +463,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       bool ok = true;
       auto sums_ready = [&](uint32_t i) { return mbar_try_wait(&acc_full[i % NACC], (i / NACC) & 1); };
       auto wait_sums = [&](uint32_t i) {
-        if (!mbar_wait(&acc_full[i % NACC], (i / NACC) & 1)) {
+        if (!mbar_wait_warp(&acc_full[i % NACC], (i / NACC) & 1)) {
           abort_now();
           ok = false;
         }
@@ -483,7 +484,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       for (int kb = kb0; kb < kb1 && ok; kb += SC_BLOCKS, ++batch) {
         const int n = min(SC_BLOCKS, kb1 - kb);
         const float* sc = s_scale + (batch & 1) * SC_FLOATS + (MODE == GATEUP || BN == 128 ? 0 : half * TM) + r;
-        if (!mbar_wait(&sc_full[batch & 1], (batch >> 1) & 1)) {
+        if (!mbar_wait_warp(&sc_full[batch & 1], (batch >> 1) & 1)) {
           abort_now();
           ok = false;
           break;
@@ -491,7 +492,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll 1
         for (int j = 0; j < n; ++j, ++it, sc += 2 * TM) {
           const float s0 = sc[0], s1 = MODE == GATEUP ? sc[TM] : s0;
-          if (!ready) {
+          if (!__all_sync(0xffffffffu, ready)) {
             wait_sums(it);
             if (!ok) break;
           }
