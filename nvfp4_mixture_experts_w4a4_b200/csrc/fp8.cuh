@@ -21,6 +21,24 @@ inline int64_t fp8_blocks(int64_t n) { return (n + FP8_BLOCK - 1) / FP8_BLOCK; }
 // infinity, so a maximum of these keeps a NaN.
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
+// A block's sum v takes two scales, a and b.  Their fp32 product serves as one factor where it is an ordinary
+// number (or either is zero).  Elsewhere it would lose bits that v * a * b need not lose, or overflow, and
+// (v * first) * second is formed: of two large scales the smaller first, of two small ones the larger, so
+// that the first product is an ordinary number wherever the result is (an infinite scale first: its sign and
+// NaN stand).
+__device__ __forceinline__ bool fp8_needs_both(float a, float b) {
+  const uint32_t p = __float_as_uint(a * b) & 0x7FFFFFFFu;
+  return p - 0x00800000u >= 0x7F000000u && a != 0.0f && b != 0.0f;
+}
+__device__ __forceinline__ void fp8_factors(float a, float b, float& first, float& second) {
+  first = 1.0f, second = a * b;
+  if (!fp8_needs_both(a, b)) return;
+  const float large = fabsf(a) >= fabsf(b) ? a : b, small = fabsf(a) >= fabsf(b) ? b : a;
+  const bool large_first = fabsf(second) < 1.0f || isinf(large);
+  first = large_first ? large : small;
+  second = large_first ? small : large;
+}
+
 // How a group divides by its scale.  fast: the scale is an ordinary number; inv approximates its
 // reciprocal to an ulp, and lo and hi are the reciprocal less and plus 2^-21 of it.  Otherwise (zero,
 // tiny, infinite or NaN maxima) elements take the slow form.

@@ -329,6 +329,9 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
   uint64_t* drain = x_full + 1;
   __shared__ uint32_t tmem_holder;
   __shared__ volatile int abort_flag;
+  // stages some of whose columns' scales do not multiply to an ordinary number: their number + 1, from the scale
+  // warp that has one, and from each adding warp once it knows
+  __shared__ volatile uint32_t s_rare[4], s_seen[8];
   __shared__ int s_active, s_scan[2][kThreads / 32], s_last;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
@@ -364,6 +367,8 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
     mbar_init(x_full, 33);
     mbar_init(drain, 1);
     abort_flag = 0;
+    for (int i = 0; i < 4; ++i) s_rare[i] = 0u;
+    for (int i = 0; i < 8; ++i) s_seen[i] = 0u;
     mbar_fence_init();
   }
   if (warp == 1) {
@@ -551,7 +556,7 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
       for (int j = u.j0; j < u.j1; ++j, ++it) {
         if (int(it % W) != warp - 12) continue;
         const int s = it % S, slot = it % kSlots;
-        float sb = 0.0f;
+        float sb = 0.0f, xs = 0.0f;
         if (u.down) {
           if (lane < 2 && 2 * j + lane < a.nI) sb = __ldg(a.w2_scale + (int64_t(e) * a.nH + u.blk) * a.nI + 2 * j + lane);
           if (u.a != have) {
@@ -566,39 +571,56 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
         } else if (lane < 2) {
           sb = __ldg(a.w13_scale + ((int64_t(e) * 2 + lane) * a.nI + u.blk) * a.nH + j);
         }
+        if (!u.down && lane < (GROUPED ? n : a.T))
+          xs = __ldg(a.x_scale + int64_t(GROUPED ? row0 + lane : lane) * a.nH + j);
         if (!mbar_wait_warp(&empty[s], ((it / S) & 1) ^ 1) ||
             !mbar_wait_warp(&acc_empty[slot], ((it / kSlots) & 1) ^ 1)) {
           abort_now();
           ok = false;
           break;
         }
+        // the columns' scales of either tile: a lane holds a column's
+        static_assert(NT <= 32, "a column a lane");
+        float cs[2] = {xs, xs};
         if (u.down) {
           if (lane == 0) {
             mbar_expect_tx(&full[s], 2 * NT * 128);
             load_tile(smem + m.h + 2 * s * NT * 128, &tmh, 2 * j * 128, row0, 0, &full[s]);
             load_tile(smem + m.h + (2 * s + 1) * NT * 128, &tmh, (2 * j + 1) * 128, row0, 0, &full[s]);
           }
-#pragma unroll
-          for (int c = lane; c < NT; c += 32) {
-            float hs[2] = {0.0f, 0.0f};
-            if (c < n) {
-              const float* q = a.h_scale + int64_t(row0 + c) * a.nI + 2 * j;
-              hs[0] = __ldcg(q);
-              if (2 * j + 1 < a.nI) hs[1] = __ldcg(q + 1);
-            }
-            s_hs[(2 * slot) * NT + c] = hs[0];
-            s_hs[(2 * slot + 1) * NT + c] = hs[1];
+          if (lane < n) {
+            const float* q = a.h_scale + int64_t(row0 + lane) * a.nI + 2 * j;
+            cs[0] = __ldcg(q);
+            if (2 * j + 1 < a.nI) cs[1] = __ldcg(q + 1);
+          }
+          if (lane < NT) {
+            s_hs[(2 * slot) * NT + lane] = cs[0];
+            s_hs[(2 * slot + 1) * NT + lane] = cs[1];
           }
         } else if constexpr (GROUPED) {
           if (lane == 0) {
             mbar_expect_tx(&full[s], NT * 128);
             load_tile(smem + m.h + 2 * s * NT * 128, &tmx, j * 128, row0, 0, &full[s]);
           }
-#pragma unroll
-          for (int c = lane; c < NT; c += 32)
-            s_hs[(2 * slot) * NT + c] = c < n ? __ldg(a.x_scale + int64_t(row0 + c) * a.nH + j) : 0.0f;
+          if (lane < NT) s_hs[(2 * slot) * NT + lane] = xs;
         }
         if (lane < 2) s_sb[2 * slot + lane] = sb;
+        const bool both = fp8_needs_both(cs[0], __shfl_sync(0xffffffffu, sb, 0)) |
+                          fp8_needs_both(cs[1], __shfl_sync(0xffffffffu, sb, 1));
+        if (__any_sync(0xffffffffu, both)) {
+          // the adding warps, held up at this stage, see its number; when all have, it may go on
+          if (lane == 0) s_rare[warp - 12] = it + 1;
+          bool seen = false;
+          for (uint32_t k = 0; k < (1u << 22) && !seen; ++k) {
+            seen = __all_sync(0xffffffffu, int32_t(s_seen[lane & 7] - (it + 1)) >= 0);
+            if (!seen) __nanosleep(64);
+          }
+          if (!seen) {
+            abort_now();
+            ok = false;
+            break;
+          }
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[s]);
       }
@@ -609,6 +631,16 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
     bool ok = GROUPED || mbar_wait_warp(x_full, 0);
     if (!ok) abort_now();
     griddep_wait();  // the counters are zero
+    auto is_rare = [&](uint32_t i) {
+      return __any_sync(0xffffffffu, s_rare[lane & 3] == i + 1) != 0;
+    };
+    auto wait_sums = [&](uint32_t i) {
+      for (uint32_t k = 0; k < (1u << 22); ++k) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(&acc_full[i % kSlots], (i / kSlots) & 1))) return true;
+        if (is_rare(i)) return false;
+      }
+      return false;
+    };
     uint32_t it = 0;
     for (int i = 0; i < units; ++i) {
       const Unit u = unit_of(p, a, i, cta);
@@ -618,28 +650,49 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
       for (int c = 0; c < NT; ++c) acc[c] = 0.0f;
       for (int j = u.j0; j < u.j1 && ok; ++j, ++it) {
         const int slot = it % kSlots;
-        if (warp_aborted() || !mbar_wait_warp(&acc_full[slot], (it / kSlots) & 1)) {
-          abort_now();
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const float sb = s_sb[2 * slot + half];
         const float4* sc = reinterpret_cast<const float4*>(
             u.down ? s_hs + (2 * slot + half) * NT : (GROUPED ? s_hs + 2 * slot * NT : s_xs + j * NT));
         constexpr int CW = NT < 32 ? NT : 32;
+        if (warp_aborted() || !wait_sums(it)) {
+          // gave up, or a rare stage: sums times one scale, then the other
+          ok = is_rare(it);
+          if (ok) {
+            if (lane == 0) s_seen[warp - 4] = it + 1;
+            ok = mbar_wait_warp(&acc_full[slot], (it / kSlots) & 1);
+          }
+          if (!ok) {
+            abort_now();
+            break;
+          }
+          tc_fence_after();
+          const float sb = s_sb[2 * slot + half];
 #pragma unroll
-        for (int c0 = 0; c0 < NT; c0 += CW) {
-          if (GROUPED && c0 >= n) break;  // columns without rows
-          uint32_t v[CW];
-          read_columns<CW>(trow + (2 * slot + half) * NT + c0, v);
+          for (int c0 = 0; c0 < NT; c0 += CW) {
+            uint32_t v[CW];
+            read_columns<CW>(trow + (2 * slot + half) * NT + c0, v);
 #pragma unroll
-          for (int c = 0; c < CW; c += 4) {
-            const float4 f = sc[(c0 + c) / 4];
-            acc[c0 + c] = fmaf(__uint_as_float(v[c]), f.x * sb, acc[c0 + c]);
-            acc[c0 + c + 1] = fmaf(__uint_as_float(v[c + 1]), f.y * sb, acc[c0 + c + 1]);
-            acc[c0 + c + 2] = fmaf(__uint_as_float(v[c + 2]), f.z * sb, acc[c0 + c + 2]);
-            acc[c0 + c + 3] = fmaf(__uint_as_float(v[c + 3]), f.w * sb, acc[c0 + c + 3]);
+            for (int c = 0; c < CW; ++c) {
+              float first, second;
+              fp8_factors(reinterpret_cast<const float*>(sc)[c0 + c], sb, first, second);
+              acc[c0 + c] = fmaf(__uint_as_float(v[c]) * first, second, acc[c0 + c]);
+            }
+          }
+        } else {
+          tc_fence_after();
+          const float sb = s_sb[2 * slot + half];
+#pragma unroll
+          for (int c0 = 0; c0 < NT; c0 += CW) {
+            if (GROUPED && c0 >= n) break;  // columns without rows
+            uint32_t v[CW];
+            read_columns<CW>(trow + (2 * slot + half) * NT + c0, v);
+#pragma unroll
+            for (int c = 0; c < CW; c += 4) {
+              const float4 f = sc[(c0 + c) / 4];
+              acc[c0 + c] = fmaf(__uint_as_float(v[c]), f.x * sb, acc[c0 + c]);
+              acc[c0 + c + 1] = fmaf(__uint_as_float(v[c + 1]), f.y * sb, acc[c0 + c + 1]);
+              acc[c0 + c + 2] = fmaf(__uint_as_float(v[c + 2]), f.z * sb, acc[c0 + c + 2]);
+              acc[c0 + c + 3] = fmaf(__uint_as_float(v[c + 3]), f.w * sb, acc[c0 + c + 3]);
+            }
           }
         }
         tc_fence_before();

@@ -74,7 +74,7 @@ constexpr int ring_bytes(int mode, int bn, bool pair) {
 }
 constexpr int amax_bytes(int mode) { return mode == GATEUP ? 2 * 2 * TM * 4 : 0; }
 constexpr int smem_bytes(int mode, int bn, bool pair) {
-  return 1024 + ring_bytes(mode, bn, pair) + (2 * stages_of(mode, bn, pair) + 2 * (512 / bn) + 5) * 8 + 16 +
+  return 1024 + ring_bytes(mode, bn, pair) + (2 * stages_of(mode, bn, pair) + 2 * (512 / bn) + 5) * 8 + 48 +
          amax_bytes(mode) + 2 * SC_FLOATS * 4;
 }
 constexpr int split_pitch(int bn) { return bn + 4; }  // floats; rows 16 bytes apart in the banks
@@ -256,6 +256,47 @@ __device__ __forceinline__ Tile tile_of(const TileParams& p, int t, int bn, bool
   return w;
 }
 
+// The columns of a warp's half: two runs of 32 a step, BN / 2 apart in a gate/up tile (its gate and up columns).
+template <int MODE, int BN>
+__device__ __forceinline__ uint32_t tile_column(int half, int c) {
+  constexpr int HALF = BN / 2;
+  if constexpr (MODE == GATEUP) return uint32_t(c < HALF / 2 ? half * (HALF / 2) + c : TM + half * (HALF / 2) + c - HALF / 2);
+  else return uint32_t(half * HALF + c);
+}
+
+// Adds n blocks' sums times one scale, then the other, read from memory again: what a batch of scales takes
+// some of whose products are no ordinary numbers.  sa, sb: the first block's (sb_up further on the up's).
+// Such a batch is held back at its barrier until every adding warp, waiting there, has seen its number, so
+// that the loop that all others take has no choice to make: with one, its reads and additions did not run
+// into one another as before (4096 x 5120 x 17408: 373 us without; a choice for every block 399 to 441, for
+// every batch 381 to 389, with this in or out of line).
+template <int MODE, int BN, bool PAIR>
+__device__ __noinline__ bool add_with_both(float* sums, const float* sa, const float* sb, int64_t sb_up, int n, uint32_t it,
+                                           uint32_t trow, int half, uint64_t* acc_full, uint64_t* acc_empty) {
+  constexpr int HALF = BN / 2;
+  constexpr uint32_t NACC = 512 / BN;
+  for (int j = 0; j < n; ++j, ++it) {
+    if (!mbar_wait_warp(&acc_full[it % NACC], (it / NACC) & 1)) return false;
+    tc_fence_after();
+#pragma unroll 1
+    for (int c = 0; c < HALF; c += 32) {
+      float first, second;
+      fp8_factors(__ldg(sa + j), __ldg(sb + j + (c >= HALF / 2 ? sb_up : 0)), first, second);
+      uint32_t v[32];
+      tmem_ld_32x32b_x32(trow + (it % NACC) * BN + tile_column<MODE, BN>(half, c), v);
+      tmem_ld_wait_for(v);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sums[c + i] = fmaf(__uint_as_float(v[i]) * first, second, sums[c + i]);
+    }
+    tc_fence_before();
+    if ((threadIdx.x & 31) == 0) {
+      if constexpr (PAIR) arrive_at(cluster_address(&acc_empty[it % NACC], 0));
+      else arrive_here(&acc_empty[it % NACC]);
+    }
+  }
+  return true;
+}
+
 template <int MODE, int BN, bool SPLIT, bool PAIR>
 __global__ void __launch_bounds__(TTHREADS, 1)
 fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -281,7 +322,10 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   uint64_t* drain = sc_empty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-  uint32_t* s_amax = reinterpret_cast<uint32_t*>(tmem_holder + 4);  // gate/up: [2][2][128]: tile parity, half, row
+  // the rare batches of scales: their number + 1, from either scale warp, and from each adding warp once it knows
+  volatile uint32_t* sc_rare = tmem_holder + 2;    // [2]
+  volatile uint32_t* rare_seen = tmem_holder + 4;  // [ADD_WARPS]
+  uint32_t* s_amax = reinterpret_cast<uint32_t*>(tmem_holder + 4 + ADD_WARPS);  // gate/up: [2][2][128]: tile parity, half, row
   float* s_scale = reinterpret_cast<float*>(s_amax + amax_bytes(MODE) / 4);  // [2][SC_BLOCKS][2][128]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -300,6 +344,8 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
+    for (int i = 0; i < 2; ++i) sc_rare[i] = 0u;
+    for (int i = 0; i < ADD_WARPS; ++i) rare_seen[i] = 0u;
     mbar_fence_init();
   }
   if (warp == 1) alloc_tmem<PAIR>(tmem_holder, 512);
@@ -400,6 +446,18 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       const int l = (warp - 2) * 32 + lane;
       uint32_t batch = 0;
       Tile next = tile_at(t_first);
+      // Whether some product of the batch's scales may be no ordinary number: by the smallest (zeros apart) and the
+      // largest of both, so it says so of some batches without one too.
+      auto rare = [&](const float (&a)[2][SC_BLOCKS], float b) {
+        uint32_t lo = 0xFFFFFFFFu, hi = 0u;  // of the magnitudes' bits, lo less one: a zero counts as large
+#pragma unroll
+        for (int j = 0; j < SC_BLOCKS; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) lo = min(lo, abs_bits(a[i][j]) - 1u), hi = max(hi, abs_bits(a[i][j]));
+        const uint32_t b_lo = __reduce_min_sync(0xffffffffu, abs_bits(b) - 1u), b_hi = __reduce_max_sync(0xffffffffu, abs_bits(b));
+        return __any_sync(0xffffffffu, fp8_needs_both(__uint_as_float(lo + 1u), __uint_as_float(b_lo + 1u)) |
+                                           fp8_needs_both(__uint_as_float(hi), __uint_as_float(b_hi))) != 0;
+      };
       for (int t = t_first; t < n_tiles && !warp_aborted(); t += t_step) {
         const Tile w = next;
         next = tile_at(t + t_step);
@@ -433,6 +491,19 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
               for (int i = 0; i < 2; ++i) dst[(j * 2 + h) * TM + 64 * i] = a[i][j] * bj;
             }
+          if (rare(a, b)) {
+            // the adding warps, held up at sc_full, see the number; when all have, the batch may go on
+            if (lane == 0) sc_rare[warp - 2] = batch + 1;
+            bool seen = false;
+            for (uint32_t i = 0; i < (1u << 22) && !seen; ++i) {
+              seen = __all_sync(0xffffffffu, int32_t(rare_seen[lane % ADD_WARPS] - (batch + 1)) >= 0);
+              if (!seen) __nanosleep(64);
+            }
+            if (!seen) {
+              abort_now();
+              break;
+            }
+          }
           mbar_arrive(&sc_full[batch & 1]);
         }
       }
@@ -443,11 +514,6 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const int half = (warp - 4) >> 2;     // its half of the columns
     const uint32_t trow = tmem + (uint32_t(q * 32) << 16);
     const uint32_t release_bar = PAIR ? cluster_address(&acc_empty[0], 0) : 0u;
-    // the two 32-column runs a step reads: gate and up columns are BN / 2 apart in a gate/up tile
-    auto column = [&](int c) -> uint32_t {
-      if constexpr (MODE == GATEUP) return uint32_t(c < HALF / 2 ? half * (HALF / 2) + c : TM + half * (HALF / 2) + c - HALF / 2);
-      else return uint32_t(half * HALF + c);
-    };
     uint32_t it = 0, batch = 0;
     int done = 0;
     for (int t = t_first; t < n_tiles && (MODE == GATEUP || !warp_aborted()); t += t_step, ++done) {
@@ -468,6 +534,14 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
           ok = false;
         }
       };
+      auto is_rare = [&](uint32_t b) { return __any_sync(0xffffffffu, sc_rare[0] == b + 1 || sc_rare[1] == b + 1) != 0; };
+      auto wait_scales = [&](uint32_t b) {
+        for (uint32_t i = 0; i < (1u << 22); ++i) {
+          if (__all_sync(0xffffffffu, mbar_try_wait(&sc_full[b & 1], (b >> 1) & 1))) return true;
+          if (is_rare(b)) return false;
+        }
+        return false;
+      };
       // The accumulator's columns have been read by this warp (tcgen05.wait::ld is the whole warp's).
       auto release_sums = [&](uint32_t i) {
         tc_fence_before();
@@ -482,12 +556,31 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       bool ready = false;
 #pragma unroll 1
       for (int kb = kb0; kb < kb1 && ok; kb += SC_BLOCKS, ++batch) {
-        const int n = min(SC_BLOCKS, kb1 - kb);
+        int n = min(SC_BLOCKS, kb1 - kb);
         const float* sc = s_scale + (batch & 1) * SC_FLOATS + (MODE == GATEUP || BN == 128 ? 0 : half * TM) + r;
-        if (!mbar_wait_warp(&sc_full[batch & 1], (batch >> 1) & 1)) {
-          abort_now();
-          ok = false;
-          break;
+        if (!wait_scales(batch)) {
+          // gave up, or a rare batch (add_with_both)
+          ok = is_rare(batch);
+          if (ok) {
+            if (lane == 0) rare_seen[warp - 4] = batch + 1;
+            const int nb = MODE == GATEUP ? w.n0 / 256 : min(w.n0 / TK + (BN == 256 ? half : 0), p.nsb - 1);
+            const float* sa = p.sa + int64_t(MODE == DENSE ? min(w.row + r, p.M - 1) : w.row + min(r, w.rows - 1)) * p.lda_s + kb;
+            const float* sb = p.sb + (MODE == GATEUP ? 2 * w.e : w.e) * p.sb_e + nb * p.ldb_s + kb;
+            float sums[HALF];
+#pragma unroll
+            for (int i = 0; i < HALF; ++i) sums[i] = acc[i];
+            ok = mbar_wait_warp(&sc_full[batch & 1], (batch >> 1) & 1) &&
+                 add_with_both<MODE, BN, PAIR>(sums, sa, sb, MODE == GATEUP ? p.sb_e : 0, n, it, trow, half, acc_full, acc_empty);
+#pragma unroll
+            for (int i = 0; i < HALF; ++i) acc[i] = sums[i];
+          }
+          if (!ok) {
+            abort_now();
+            break;
+          }
+          it += n;
+          n = 0;
+          ready = false;
         }
 #pragma unroll 1
         for (int j = 0; j < n; ++j, ++it, sc += 2 * TM) {
@@ -501,7 +594,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
             for (int c = 0; c < HALF; c += 32) {
               uint32_t v[32];
-              tmem_ld_32x32b_x32(trow + (it % NACC) * BN + column(c), v);
+              tmem_ld_32x32b_x32(trow + (it % NACC) * BN + tile_column<MODE, BN>(half, c), v);
               tmem_ld_wait_for(v);
               if (c + 32 == HALF) {
                 release_sums(it);

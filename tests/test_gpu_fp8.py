@@ -815,3 +815,52 @@ def test_graphs_refuse_replaced_weights(T):
     fp4.w.w2_sf = fp4.w.w2_sf.clone()
     with pytest.raises(RuntimeError, match="w2_sf"):
         graph(x, logits[:, :4])
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 40, 64), (77, 300, 1003), (40, 96, 4000), (1300, 4200, 300)])
+@pytest.mark.parametrize("ea,eb", [(-100, -38), (-20, -115), (-110, -40), (70, 60), (30, 97), (100, -100), (-90, 100)])
+def test_gemm_scales_of_any_size(M, N, K, ea, eb):
+    """Scales whose product is below the smallest ordinary fp32 number or above the largest, where D is
+    neither: the codes are made large or small to match.  (2^-149 an addition where a block's share is no
+    ordinary number.)"""
+    a, sa, b, sb = matrices(M, N, K, M + K)
+    if ea + eb > 64:   # codes of at most 2^-5: a block's sum is below 2^-2
+        a, b = ((t.float() * 2.0 ** -14).to(torch.float8_e4m3fn) for t in (a, b))
+        a, b = (torch.nn.functional.pad(t.view(torch.uint8), (0, -K % 16))[:, :K].view(torch.float8_e4m3fn) for t in (a, b))
+    sa, sb = sa / sa.amax() * 1.37 * 2.0 ** ea, sb / sb.amax() * 1.23 * 2.0 ** eb
+    sa[:, ::3] *= 2.0 ** -5      # a row's blocks, and an accumulator's rows, on both sides of the border
+    sa[::2] *= 2.0 ** 4
+    d = ops.fp8_gemm(a, sa, b, sb, out_dtype=torch.float32)
+    A, B = a.double() * spread(sa.double(), 1, a.shape), b.double() * spread(sb.double(), 128, b.shape)
+    ref, size = A @ B.T, A.abs() @ B.abs().T
+    bound = (4 * 128 + blocks(K) + 3) * 2.0 ** -24 * size + F32_HALF * ref.abs() + (blocks(K) + 1) * 2.0 ** -149
+    most = torch.finfo(torch.float32).max
+    fits = ref.abs() + bound < most
+    assert fits.any() and ((d.double() - ref).abs() <= bound)[fits].all()
+
+
+@pytest.mark.parametrize("T", [5, 40, 300])
+@pytest.mark.parametrize("ex,eg,eu,ed", [(-100, -30, 120, 60), (-60, -70, 110, 60), (0, 0, -91, -36), (100, 50, -110, -60)])
+def test_layer_scales_of_any_size(T, ex, eg, eu, ed):
+    """x and weights whose scales' products are no ordinary numbers: 2^(ex + eg) for the gate, 2^(ex + eu) for
+    the up and, of h's size, by 2^ed for the down.  Where the gate's is above the largest, weights meet the small
+    elements of x alone, so that the sums are not."""
+    H, I = 336, 208
+    g = gen(T)
+    x, logits = torch.randn(T, H, generator=g, device="cuda"), torch.randn(T, 3, generator=g, device="cuda")
+    w = [torch.randn(3, I, H, generator=g, device="cuda") / math.sqrt(H) for _ in range(2)]
+    w = ops.FP8Experts.from_float(*w, torch.randn(3, H, I, generator=g, device="cuda") / math.sqrt(I))
+    codes, s = w.w13_codes.view(torch.uint8).clone(), w.w13_scale.clone()
+    if ex + eg > 128:
+        x *= 2.0 ** -16
+        x[:, ::16] = 1.0
+        codes[..., ::16] = 0
+        codes = (codes.view(torch.float8_e4m3fn).float() * 2.0 ** -14).to(torch.float8_e4m3fn)
+    s[:, 0] *= 2.0 ** eg
+    s[:, 1] *= 2.0 ** eu
+    w = ops.FP8Experts(codes, s, w.w2_codes, w.w2_scale * 2.0 ** ed)
+    x = (x * 2.0 ** ex).bfloat16()
+    y = ops.FP8MoeFFN(w, 2)(x, logits)
+    assert y.isfinite().all() and (y != 0).any()
+    ref, bound = layer_reference(w, x, logits, 2, False)
+    assert ((y.double() - ref).abs() <= bound + 2.0 ** -134).all()   # half of bf16's last step
