@@ -39,6 +39,14 @@ __device__ __forceinline__ void fp8_factors(float a, float b, float& first, floa
   second = large_first ? small : large;
 }
 
+// silu(g) u by e^-|g|, which is at most 1: 1 + e^-g leaves fp32's range (or the fast division's, 2^126) where
+// the result need not.  The fast exponential is off by 2 + 1.2 |g| of 2^-23 (2^-19 at |g| = 12, 2^-17 at 88), before
+// codes whose step is 2^-4 and more: expf took 138.0 us where this takes 134.0 (512 tokens, 512 experts 2048 x 512).
+__device__ __forceinline__ float silu_times(float g, float u) {
+  const float e = __expf(-fabsf(g));
+  return __fdividef(g < 0.0f ? g * e : g, 1.0f + e) * u;
+}
+
 // How a group divides by its scale.  fast: the scale is an ordinary number; inv approximates its
 // reciprocal to an ulp, and lo and hi are the reciprocal less and plus 2^-21 of it.  Otherwise (zero,
 // tiny, infinite or NaN maxima) elements take the slow form.

@@ -747,7 +747,7 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
           if (half == 0) {
 #pragma unroll
             for (int c = 0; c < NT; ++c)
-              s_buf[c * kPitch + r] = __fdividef(acc[c], 1.0f + __expf(-acc[c])) * s_buf[c * kPitch + r];
+              s_buf[c * kPitch + r] = silu_times(acc[c], s_buf[c * kPitch + r]);
           }
           add_barrier();
           // a warp takes every eighth token of the expert: 128 columns, one group

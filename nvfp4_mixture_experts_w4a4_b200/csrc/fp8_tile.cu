@@ -637,7 +637,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
           u[0] = acc[HALF / 2 + 2 * i], u[1] = acc[HALF / 2 + 2 * i + 1];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            h[2 * i + j] = __fdividef(g[j], 1.0f + __expf(-g[j])) * u[j];
+            h[2 * i + j] = silu_times(g[j], u[j]);
             m = max(m, abs_bits(h[2 * i + j]));
           }
         }

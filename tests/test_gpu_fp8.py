@@ -864,3 +864,25 @@ def test_layer_scales_of_any_size(T, ex, eg, eu, ed):
     assert y.isfinite().all() and (y != 0).any()
     ref, bound = layer_reference(w, x, logits, 2, False)
     assert ((y.double() - ref).abs() <= bound + 2.0 ** -134).all()   # half of bf16's last step
+
+
+@pytest.mark.parametrize("T", [5, 40, 300])
+@pytest.mark.parametrize("gate", [-20.0, -80.0, -87.8, -88.5, -95.0, 30.0, 95.0])
+def test_layer_gates_far_from_zero(T, gate):
+    """silu(g) u where e^-g leaves fp32's range: x has one element, so g is the one product within 2^-22 of it
+    (88 * 2^-22 of the exponential, below 2^-14), u (2^120 at most) brings h back towards one, and all of a row's h are equal
+    (code 448, exact).  2^-12 of the exponential where it is below the ordinary numbers (-95: 2^-137, in steps
+    of 2^-149), half a step of bf16 for the output."""
+    H, I = 256, 128
+    x = torch.zeros(T, H, device="cuda", dtype=torch.bfloat16)
+    x[:, 3] = 1.0
+    silu = gate / (1 + math.exp(-gate))
+    wg, wu = torch.zeros(1, I, H, device="cuda"), torch.zeros(1, I, H, device="cuda")
+    wg[..., 3], wu[..., 3] = gate, math.copysign(min(1 / abs(silu), 2.0 ** 120), silu)
+    w = ops.FP8Experts.from_float(wg, wu, torch.eye(I, device="cuda").repeat(2, 1)[None])
+    y = ops.FP8MoeFFN(w, 1)(x, torch.zeros(T, 1, device="cuda"))
+    g = w.w13_scale[0, 0, 0, 0].double() * 448 * math.copysign(1, gate)
+    u = w.w13_scale[0, 1, 0, 0].double() * 448 * math.copysign(1, silu)
+    want = g / (1 + torch.exp(-g)) * u
+    slack = 2.0 ** -14 + (2.0 ** -12 if gate < -87.3 else 0.0) + BF16_HALF * (1 + 2.0 ** -7)
+    assert ((y.double() - want).abs() <= slack * want.abs()).all()
