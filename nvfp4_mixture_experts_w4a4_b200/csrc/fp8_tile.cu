@@ -304,7 +304,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   constexpr int STAGES = stages_of(MODE, BN, PAIR);
   constexpr int B_ROWS = b_rows(BN, PAIR);
   constexpr int B_STAGE = B_ROWS * TK;
-  static_assert(!PAIR || (BN == 256 && !SPLIT), "a pair runs 256 x 256 tiles, whole sums");
+  static_assert(!PAIR || (MODE == DENSE && BN == 256 && !SPLIT), "a pair runs 256 x 256 tiles of a dense product, whole sums");
   constexpr int HALF = BN / 2;          // columns an adding warp holds
   constexpr uint32_t NACC = 512 / BN;   // accumulators: all of TMEM
   constexpr bool GROUPED = MODE != DENSE;
@@ -399,9 +399,7 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
           if (side == 0) mbar_arrive_expect_tx(&full[s], all_boxes * p.a_box * TK + CTAS * B_STAGE);
           for (int b = 0; b < boxes; ++b)
             load_box<PAIR>(sA + s * A_STAGE + b * p.a_box * TK, &tmA, kb * TK, w.row + side * TM + b * p.a_box, 0, bar);
-          if constexpr (MODE == GATEUP && PAIR) {
-            load_box<PAIR>(sB + s * B_STAGE, &tmB, kb * TK, w.n0 / 2, 2 * w.e + side, bar);
-          } else if constexpr (MODE == GATEUP) {
+          if constexpr (MODE == GATEUP) {
             load_box<PAIR>(sB + s * B_STAGE, &tmB, kb * TK, w.n0 / 2, 2 * w.e, bar);
             load_box<PAIR>(sB + s * B_STAGE + TM * TK, &tmB, kb * TK, w.n0 / 2, 2 * w.e + 1, bar);
           } else {
