@@ -202,7 +202,7 @@ __device__ __forceinline__ void place_fp8(const BatchArgs& a, int t0, int nt, co
 }
 
 // {expert, first row, rows} for every `group` rows of every expert, [0].x their number, and a zeroed
-// counter for each.
+// counter for each where there are counters.
 __device__ __forceinline__ void list_groups(const Fp8Place& p, int E, const int32_t* s_first, const int32_t* s_cnt,
                                             int32_t* s_sum) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -233,7 +233,8 @@ __device__ __forceinline__ void list_groups(const Fp8Place& p, int E, const int3
     for (int r = 0; r < n[i]; r += p.group)
       p.groups[1 + at++] = make_int4(2 * int(threadIdx.x) + i, first[i] + r, min(p.group, n[i] - r), 0);
   if (threadIdx.x == 0) p.groups[0] = make_int4(total, 0, 0, 0);
-  for (int i = threadIdx.x; i < total; i += kThreads) p.counters[i] = 0;
+  if (p.counters)
+    for (int i = threadIdx.x; i < total; i += kThreads) p.counters[i] = 0;
 }
 
 template <bool FP8>

@@ -97,7 +97,7 @@ struct Fp8Place {  // the FP8 layer: x in E4M3 in expert order, and the row grou
   float* scale;      // [pairs][ceil(H / 128)]
   int group;         // rows of a group
   int4* groups;      // [0].x their number, then {expert, first row, rows, -} each
-  int* counters;     // one for each group, zeroed
+  int* counters;     // nullable: one for each group, zeroed
 };
 bool batch_prologue_fits(int T, int E, int k);
 int64_t batch_prologue_scratch_bytes(int T, int E);

@@ -15,7 +15,7 @@ constexpr int kRowTile = 128;  // rows of a tile of the grouped products
 // x [T][H] bf16 -> E4M3 rows in expert order: each 128-element group is quantised once (half a
 // warp, 16 bytes a lane) and written to the k rows of its token.  Block 0 writes the list of row
 // groups instead ({expert, first row, rows} for every `group` rows of every expert, [0].x their number) and
-// zeroes a counter for each.
+// zeroes a counter for each where there are counters.
 __global__ void __launch_bounds__(kPlaceThreads)
 fp8_place_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ pair_to_row,
                  const int32_t* __restrict__ offsets, int T, int H, int E, int k, uint8_t* __restrict__ codes,
@@ -51,7 +51,8 @@ fp8_place_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict_
 #pragma unroll
     for (int i = 0; i < PER; ++i)
       for (int r = 0; r < n[i]; r += group) tiles[1 + at++] = make_int4(e0 + i, first[i] + r, min(group, n[i] - r), 0);
-    for (int i = threadIdx.x; i < total; i += kPlaceThreads) counters[i] = 0;
+    if (counters)
+      for (int i = threadIdx.x; i < total; i += kPlaceThreads) counters[i] = 0;
     if (threadIdx.x == 0) tiles[0] = make_int4(total, 0, 0, 0);
     return;
   }
@@ -157,7 +158,7 @@ Layout make_layout(const fp8_moe_ffn_desc& d) {
   L.active = put((d.E + 1) * 4);
   L.scratch = put(d.T > 0 ? batch_prologue_scratch_bytes(d.T, d.E) : 0);
   L.groups = put((int64_t(L.max_row_tiles) + 1) * 16);
-  L.counters = put(int64_t(L.max_row_tiles) * 4);
+  L.counters = L.stream ? put(int64_t(L.max_row_tiles) * 4) : 0;  // (the tiles count nothing)
   L.x_codes = put(P * d.H), L.x_scale = put(P * nH * 4);
   L.h_codes = put(P * d.I), L.h_scale = put(P * nI * 4);
   L.slots = put(P * d.H * 4);
@@ -207,6 +208,7 @@ nvfp4moe_status fp8_moe_ffn_forward(const fp8_moe_ffn_desc* desc, const void* x,
     return launch_fp8_layer(c, s);
   }
   int4* groups = reinterpret_cast<int4*>(ws + L.groups);
+  int* counters = L.stream ? i32(L.counters) : nullptr;
   if (prologue_fits(d.T, d.E, d.top_k)) {
     // one cluster launch for routing and permutation, then x
     st = launch_prologue(x, logits, d.T, d.H, d.E, d.top_k, 1, 0, nullptr, i32(L.ids), f32(L.w), i32(L.counts),
@@ -218,10 +220,10 @@ nvfp4moe_status fp8_moe_ffn_forward(const fp8_moe_ffn_desc* desc, const void* x,
                          dim3(kPlaceThreads), 0, s, static_cast<const __nv_bfloat16*>(x),
                          static_cast<const int32_t*>(i32(L.pair_to_row)), static_cast<const int32_t*>(i32(L.offsets)),
                          int(d.T), int(d.H), int(d.E), int(d.top_k), ws + L.x_codes, f32(L.x_scale), L.group, groups,
-                         i32(L.counters));
+                         counters);
     NVFP4_REQUIRE(e == cudaSuccess, NVFP4MOE_CUDA_ERROR, "%s: %s", fn, cudaGetErrorString(e));
   } else {
-    const Fp8Place place{ws + L.x_codes, f32(L.x_scale), L.group, groups, i32(L.counters)};
+    const Fp8Place place{ws + L.x_codes, f32(L.x_scale), L.group, groups, counters};
     st = launch_batch_prologue(x, logits, d.T, d.H, d.E, d.top_k, 1, 0, nullptr, i32(L.ids), f32(L.w), i32(L.counts),
                                i32(L.offsets), i32(L.padded), i32(L.pair_to_row), i32(L.row_token), i32(L.row_pair),
                                i32(L.tile_expert), i32(L.active), nullptr, 1, nullptr, nullptr, ws + L.scratch, nullptr,
@@ -236,7 +238,7 @@ nvfp4moe_status fp8_moe_ffn_forward(const fp8_moe_ffn_desc* desc, const void* x,
   g.x_codes = ws + L.x_codes, g.x_scale = f32(L.x_scale);
   g.w13_codes = d.w13_codes, g.w13_scale = d.w13_scale, g.w2_codes = d.w2_codes, g.w2_scale = d.w2_scale;
   g.h_codes = ws + L.h_codes, g.h_scale = f32(L.h_scale), g.slots = f32(L.slots);
-  st = L.stream ? launch_fp8_stream(g, i32(L.counters), s) : launch_fp8_grouped(g, s);
+  st = L.stream ? launch_fp8_stream(g, counters, s) : launch_fp8_grouped(g, s);
   if (st != NVFP4MOE_OK) return st;
   return launch_combine_rows(f32(L.slots), i32(L.pair_to_row), f32(L.w), d.T, d.H, d.top_k, out, s);
 }
