@@ -886,3 +886,19 @@ def test_layer_gates_far_from_zero(T, gate):
     want = g / (1 + torch.exp(-g)) * u
     slack = 2.0 ** -14 + (2.0 ** -12 if gate < -87.3 else 0.0) + BF16_HALF * (1 + 2.0 ** -7)
     assert ((y.double() - want).abs() <= slack * want.abs()).all()
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [
+    (1300, 4200, 300), (2000, 5000, 1003), (1536, 4000, 1200), (300, 7001, 2304),  # pairs of CTAs
+    (16, 24576, 1536), (100, 20000, 700), (90, 24001, 400),                        # 256 columns, whole sums
+    (2311, 432, 2969), (2953, 140, 7046), (30, 18500, 9000),                       # 256 columns, split sums
+])
+def test_gemm_in_wide_tiles(M, N, K, out_dtype):
+    """Sums of several blocks, scales of more than one batch of eight, and sizes that end inside a block or
+    tile, for the forms that 148 SMs give these sizes."""
+    a, sa, b, sb = matrices(M, N, K, M + K)
+    d = ops.fp8_gemm(a, sa, b, sb, out_dtype=out_dtype)
+    check_gemm(d, a, sa, b, sb)
+    assert torch.equal(d, ops.fp8_gemm(a, sa, b, sb, out_dtype=out_dtype))
+    assert ops.device_status() == 0
