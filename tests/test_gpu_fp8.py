@@ -902,3 +902,32 @@ def test_gemm_in_wide_tiles(M, N, K, out_dtype):
     check_gemm(d, a, sa, b, sb)
     assert torch.equal(d, ops.fp8_gemm(a, sa, b, sb, out_dtype=out_dtype))
     assert ops.device_status() == 0
+
+
+@pytest.mark.parametrize("T", [1, 16, 40, 300])
+def test_weights_written_right_before_a_call(T):
+    """The layer reads weights, scales and logits that the launches right before it wrote in place."""
+    g = gen(T)
+    E, I, H = 6, 256, 512
+    ws = [[torch.randn(E, *s, generator=g, device="cuda") / math.sqrt(s[1]) for s in ((I, H), (I, H), (H, I))] for _ in range(2)]
+    fixed = [ops.FP8Experts.from_float(*w) for w in ws]
+    w = ops.FP8Experts.from_float(*ws[0])
+    layer = ops.FP8MoeFFN(w, 2)
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    router, sr = ops.fp8_quantize(torch.randn(E, H, generator=g, device="cuda"), tile=ops.FP8_BLOCKS)
+    codes, scale = ops.fp8_quantize(x)
+    logits = ops.fp8_gemm(codes, scale, router, sr, out_dtype=torch.float32)
+    want = [[ops.FP8MoeFFN(f, 2)(x, l) for l in (logits, -logits)] for f in fixed]
+    torch.cuda.synchronize()
+    now, minus = torch.empty_like(logits), torch.full_like(logits, -1.0)
+    for i in range(24):
+        a, b = i & 1, i >> 1 & 1
+        for n, (c, s) in enumerate(((w.w13_codes[:, 0], w.w13_scale[:, 0]), (w.w13_codes[:, 1], w.w13_scale[:, 1]),
+                                    (w.w2_codes, w.w2_scale))):
+            ops.fp8_quantize(ws[a][n], tile=ops.FP8_BLOCKS, codes=c, scale=s)
+        ops.fp8_gemm(codes, scale, router, sr, out=now)
+        if b:
+            now.mul_(minus)
+            ops.fp8_quantize(ws[a][2], tile=ops.FP8_BLOCKS, codes=w.w2_codes, scale=w.w2_scale)
+        assert torch.equal(layer(x, now), want[a][b]), i
+    assert ops.device_status() == 0
