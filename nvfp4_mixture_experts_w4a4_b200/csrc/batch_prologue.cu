@@ -169,26 +169,16 @@ __device__ __forceinline__ void place_fp8(const BatchArgs& a, int t0, int nt, co
       const int col = b * FP8_BLOCK + (sub + 4 * j) * 8;
       u[j] = g0 < groups && col < a.H ? __ldg(reinterpret_cast<const uint4*>(a.x + int64_t(t0 + tl) * a.H + col))
                                       : make_uint4(0u, 0u, 0u, 0u);
-      m = __vmaxu2(m, __vmaxu2(__vmaxu2(u[j].x & 0x7FFF7FFFu, u[j].y & 0x7FFF7FFFu),
-                               __vmaxu2(u[j].z & 0x7FFF7FFFu, u[j].w & 0x7FFF7FFFu)));
+      m = bf16x8_max(m, u[j]);
     }
-    m = max(m << 16, m & 0xFFFF0000u);
+    m = fp8_amax_bits(m);
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     const Fp8ScaleBf16 f = fp8_scale_bf16(m);
     if (g0 >= groups) continue;
     uint2 w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t q[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(q[i] << 16);
-        v[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
-      }
-      w[j] = make_uint2(fp8_encode4(v, f), fp8_encode4(v + 4, f));
-    }
+    for (int j = 0; j < 4; ++j) w[j] = fp8_encode8(u[j], f);
     for (int d = 0; d < a.k; ++d) {
       const int64_t row = s_row[tl * a.k + d];
 #pragma unroll
@@ -199,42 +189,6 @@ __device__ __forceinline__ void place_fp8(const BatchArgs& a, int t0, int nt, co
       if (sub == 0) a.fp8.scale[row * nb + b] = f.scale;
     }
   }
-}
-
-// {expert, first row, rows} for every `group` rows of every expert, [0].x their number, and a zeroed
-// counter for each where there are counters.
-__device__ __forceinline__ void list_groups(const Fp8Place& p, int E, const int32_t* s_first, const int32_t* s_cnt,
-                                            int32_t* s_sum) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int first[2], n[2], mine = 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int e = 2 * int(threadIdx.x) + i;
-    first[i] = e < E ? s_first[e] : 0;
-    n[i] = e < E ? s_cnt[e] : 0;
-    mine += (n[i] + p.group - 1) / p.group;
-  }
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  __syncthreads();  // the scratch was read before
-  if (lane == 31) s_sum[warp] = incl;
-  __syncthreads();
-  int at = incl - mine, total = 0;
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) at += s_sum[w];
-    total += s_sum[w];
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    for (int r = 0; r < n[i]; r += p.group)
-      p.groups[1 + at++] = make_int4(2 * int(threadIdx.x) + i, first[i] + r, min(p.group, n[i] - r), 0);
-  if (threadIdx.x == 0) p.groups[0] = make_int4(total, 0, 0, 0);
-  if (p.counters)
-    for (int i = threadIdx.x; i < total; i += kThreads) p.counters[i] = 0;
 }
 
 template <bool FP8>
@@ -359,7 +313,9 @@ __global__ void __launch_bounds__(kThreads) place_quant_kernel(BatchArgs a) {
 
   if constexpr (FP8) {
     place_fp8(a, t0, nt, s_row);
-    if (c == int(gridDim.x) - 1) list_groups(a.fp8, E, s_poff, s_cnt, s_w32);
+    if (c == int(gridDim.x) - 1)
+      fp8_list_groups<kThreads>(E, a.fp8.group, [&](int e) { return s_poff[e]; }, [&](int e) { return s_cnt[e]; }, s_w32,
+                                a.fp8.groups, a.fp8.counters);
     return;  // rows are not padded
   }
 

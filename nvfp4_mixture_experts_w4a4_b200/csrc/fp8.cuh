@@ -145,4 +145,59 @@ __device__ __forceinline__ uint32_t fp8_encode4(const float* v, const Fp8ScaleBf
   return e4m3x2_from_f32(q[0], q[1]) | (e4m3x2_from_f32(q[2], q[3]) << 16);
 }
 
+// The list of row groups that the expert products run over, by one CTA of THREADS threads: {expert, first row,
+// rows, -} for every `group` rows of every expert from groups[1] on, groups[0].x their number, and a zeroed
+// counter for each where there are counters.  first(e), rows(e) of an expert; s_sum: a word a warp.
+template <int THREADS, typename First, typename Rows>
+__device__ __forceinline__ void fp8_list_groups(int E, int group, First first, Rows rows, int* s_sum, int4* groups,
+                                                int* counters) {
+  constexpr int PER = 1024 / THREADS;  // at most 1024 experts
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = int(threadIdx.x) * PER;
+  int from[PER], n[PER], mine = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    from[i] = e0 + i < E ? first(e0 + i) : 0;
+    n[i] = e0 + i < E ? rows(e0 + i) : 0;
+    mine += (n[i] + group - 1) / group;
+  }
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();  // the scratch was read before
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  int at = incl - mine, total = 0;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) at += s_sum[w];
+    total += s_sum[w];
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    for (int r = 0; r < n[i]; r += group) groups[1 + at++] = make_int4(e0 + i, from[i] + r, min(group, n[i] - r), 0);
+  if (threadIdx.x == 0) groups[0] = make_int4(total, 0, 0, 0);
+  if (counters)
+    for (int i = threadIdx.x; i < total; i += THREADS) counters[i] = 0;
+}
+
+// Eight bf16 elements as they are in memory: the largest magnitudes of them and of m, as pairs of bf16 bits
+// (fp8_amax_bits: the larger of a pair as fp32 bits), and their codes.
+__device__ __forceinline__ uint32_t bf16x8_max(uint32_t m, const uint4& q) {
+  m = __vmaxu2(m, __vmaxu2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu));
+  return __vmaxu2(m, __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu));
+}
+__device__ __forceinline__ uint32_t fp8_amax_bits(uint32_t pair) { return max(pair << 16, pair & 0xFFFF0000u); }
+__device__ __forceinline__ uint2 fp8_encode8(const uint4& q, const Fp8ScaleBf16& f) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+  return make_uint2(fp8_encode4(v, f), fp8_encode4(v + 4, f));
+}
+
 }  // namespace nvfp4moe

@@ -14,46 +14,17 @@ constexpr int kRowTile = 128;  // rows of a tile of the grouped products
 
 // x [T][H] bf16 -> E4M3 rows in expert order: each 128-element group is quantised once (half a
 // warp, 16 bytes a lane) and written to the k rows of its token.  Block 0 writes the list of row
-// groups instead ({expert, first row, rows} for every `group` rows of every expert, [0].x their number) and
-// zeroes a counter for each where there are counters.
+// groups instead.
 __global__ void __launch_bounds__(kPlaceThreads)
 fp8_place_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ pair_to_row,
                  const int32_t* __restrict__ offsets, int T, int H, int E, int k, uint8_t* __restrict__ codes,
                  float* __restrict__ scale, int group, int4* __restrict__ tiles, int* __restrict__ counters) {
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (blockIdx.x == 0) {
     __shared__ int s_sum[kPlaceThreads / 32];
-    constexpr int PER = 1024 / kPlaceThreads;
-    const int e0 = threadIdx.x * PER;
-    int first[PER], n[PER], mine = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = e0 + i;
-      first[i] = e < E ? offsets[e] : 0;
-      n[i] = e < E ? offsets[e + 1] - first[i] : 0;
-      mine += (n[i] + group - 1) / group;
-    }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) s_sum[warp] = incl;
-    __syncthreads();
-    int at = incl - mine, total = 0;
-    for (int w = 0; w < kPlaceThreads / 32; ++w) {
-      if (w < warp) at += s_sum[w];
-      total += s_sum[w];
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      for (int r = 0; r < n[i]; r += group) tiles[1 + at++] = make_int4(e0 + i, first[i] + r, min(group, n[i] - r), 0);
-    if (counters)
-      for (int i = threadIdx.x; i < total; i += kPlaceThreads) counters[i] = 0;
-    if (threadIdx.x == 0) tiles[0] = make_int4(total, 0, 0, 0);
+    fp8_list_groups<kPlaceThreads>(E, group, [&](int e) { return offsets[e]; },
+                                   [&](int e) { return offsets[e + 1] - offsets[e]; }, s_sum, tiles, counters);
     return;
   }
   const int nb = (H + FP8_BLOCK - 1) / FP8_BLOCK;
@@ -62,24 +33,13 @@ fp8_place_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict_
   const int sub = threadIdx.x & 15;
   const int64_t t = g / nb;
   const int b = int(g - t * nb), c = b * FP8_BLOCK + sub * 8;
-  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   const bool live = g < groups && c < H;  // H is a multiple of 16: eight elements exist or none
-  if (live) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(x + t * H + c));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    }
-  }
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
+  const uint4 u = live ? __ldg(reinterpret_cast<const uint4*>(x + t * H + c)) : make_uint4(0u, 0u, 0u, 0u);
+  uint32_t m = fp8_amax_bits(bf16x8_max(0u, u));
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   const Fp8ScaleBf16 f = fp8_scale_bf16(m);
-  const uint2 out = make_uint2(fp8_encode4(v, f), fp8_encode4(v + 4, f));
+  const uint2 out = fp8_encode8(u, f);
   if (!live) return;
   for (int j = 0; j < k; ++j) {
     const int64_t row = __ldg(pair_to_row + t * k + j);

@@ -189,14 +189,6 @@ __device__ __forceinline__ void load_tile(void* dst, const CUtensorMap* map, int
       ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}"
-      ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate), "r"(0u)
-      : "memory");
-}
 __device__ __forceinline__ int load_acquire(const int* p) {
   int v;
   asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
@@ -231,19 +223,6 @@ __device__ __forceinline__ bool wait_count_warp(const int* p, int want) {
   return false;
 }
 __device__ __forceinline__ void add_barrier() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-// A barrier of the adding warps that tells each whether any of them gave up waiting.  They leave their
-// units together: one that left alone would not come to the next barrier.
-__device__ __forceinline__ bool add_barrier_any(bool gave_up) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 256, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(uint32_t(gave_up))
-      : "memory");
-  return r != 0;
-}
-
 template <int N>
 __device__ __forceinline__ void read_columns(uint32_t taddr, uint32_t (&r)[N]) {
   if constexpr (N == 32) {
@@ -270,17 +249,15 @@ fp8_layer_prepare_kernel(const __nv_bfloat16* __restrict__ x, int T, int H, uint
   const int nH = ceil_div(H, 128), sub = threadIdx.x & 7;
   const int g = (blockIdx.x * 256 + threadIdx.x) >> 3;
   const int t = g / nH, kb = g - t * nH;
-  uint32_t u[2][4], mx = 0;
+  uint4 u[2];
+  uint32_t mx = 0;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int c = kb * 128 + (sub + 8 * j) * 8;
-    uint4 q = make_uint4(0u, 0u, 0u, 0u);
-    if (t < T && c < H) q = __ldg(reinterpret_cast<const uint4*>(x + int64_t(t) * H + c));
-    u[j][0] = q.x, u[j][1] = q.y, u[j][2] = q.z, u[j][3] = q.w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) mx = __vmaxu2(mx, u[j][i] & 0x7FFF7FFFu);
+    u[j] = t < T && c < H ? __ldg(reinterpret_cast<const uint4*>(x + int64_t(t) * H + c)) : make_uint4(0u, 0u, 0u, 0u);
+    mx = bf16x8_max(mx, u[j]);
   }
-  mx = max(mx << 16, mx & 0xFFFF0000u);
+  mx = fp8_amax_bits(mx);
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   const Fp8ScaleBf16 f = fp8_scale_bf16(mx);
@@ -288,18 +265,8 @@ fp8_layer_prepare_kernel(const __nv_bfloat16* __restrict__ x, int T, int H, uint
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int c = kb * 128 + (sub + 8 * j) * 8;
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float v[4];
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        v[2 * q] = __uint_as_float(u[j][2 * i + q] << 16);
-        v[2 * q + 1] = __uint_as_float(u[j][2 * i + q] & 0xFFFF0000u);
-      }
-      w[i] = fp8_encode4(v, f);
-    }
-    if (c < H) *reinterpret_cast<uint2*>(codes + int64_t(t) * H + c) = make_uint2(w[0], w[1]);
+    const uint2 w = fp8_encode8(u[j], f);
+    if (c < H) *reinterpret_cast<uint2*>(codes + int64_t(t) * H + c) = w;
   }
   if (sub == 0) scale[t * nH + kb] = f.scale;
 }
@@ -500,7 +467,7 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
     }
   } else if (warp == 1) {
     if (elect_one()) {
-      constexpr uint32_t idesc = (1u << 4) | (uint32_t(NT >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+      constexpr uint32_t idesc = idesc_f8(128, NT);
       uint32_t it = 0;
       bool ok = GROUPED || mbar_wait(x_full, 0);
       if (!ok) abort_now();
@@ -522,7 +489,7 @@ fp8_layer_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant
             const uint64_t bd = desc_kmajor_sw128(b);
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              mma_f8(tmem + (2 * slot + h) * NT, ad + 2 * q, bd + 2 * q, idesc, q != 0 ? 1u : 0u);
+              tc_mma_f8(tmem + (2 * slot + h) * NT, ad + 2 * q, bd + 2 * q, idesc, q != 0 ? 1u : 0u);
           }
           tc_commit(&empty[s]);
           tc_commit(&acc_full[slot]);

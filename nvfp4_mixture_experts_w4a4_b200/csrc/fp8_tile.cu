@@ -122,23 +122,15 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-template <bool PAIR>
-__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  if constexpr (PAIR)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, {%5, %5, %5, %5, %5, %5, %5, %5}, p;\n\t}"
-        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(0u)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, {%5, %5, %5, %5}, p;\n\t}"
-        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(0u)
-        : "memory");
+// The same instruction as tc_mma_f8 over a pair's two shared memories and TMEMs.
+__device__ __forceinline__ void tc_mma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, {%5, %5, %5, %5, %5, %5, %5, %5}, p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(0u)
+      : "memory");
 }
 
 // Arrives on `bar` (PAIR: in both CTAs) once every MMA issued so far by this thread has completed.
@@ -170,12 +162,6 @@ __device__ __forceinline__ void free_tmem(uint32_t taddr, uint32_t ncols) {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
   else
     tmem_dealloc(taddr, ncols);
-}
-
-// kind::f8f6f4 instruction descriptor: fp32 accumulator (bits [4,6) = 1), E4M3 A and B (bits
-// [7,10) and [10,13) = 0), both K-major, N >> 3 at bit 17, M >> 4 at bit 24.
-constexpr uint32_t idesc_f8(int M, int N) {
-  return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
 
 // tcgen05.wait::ld that the registers of the load pass through, so that no use of them can be moved
@@ -210,19 +196,6 @@ __device__ __forceinline__ void reg_give() {
 template <int N>
 __device__ __forceinline__ void reg_take() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-// A barrier of the adding warps that tells each whether any of them gave up waiting.  They leave their
-// units together: one that left alone would not come to the next barrier.
-__device__ __forceinline__ bool add_barrier_any(bool gave_up) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 256, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(uint32_t(gave_up))
-      : "memory");
-  return r != 0;
 }
 
 struct Tile {
@@ -431,8 +404,10 @@ fp8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
           const uint64_t a_d = desc_kmajor_sw128(sA + s * A_STAGE);
           const uint64_t b_d = desc_kmajor_sw128(sB + s * B_STAGE);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)  // K = 32 per MMA: 32 bytes = 2 descriptor units
-            tc_mma_f8<PAIR>(tmem + ab * BN, a_d + 2 * j, b_d + 2 * j, idesc, j != 0 ? 1u : 0u);
+          for (int j = 0; j < 4; ++j) {  // K = 32 per MMA: 32 bytes = 2 descriptor units
+            if constexpr (PAIR) tc_mma_f8_pair(tmem + ab * BN, a_d + 2 * j, b_d + 2 * j, idesc, j != 0 ? 1u : 0u);
+            else tc_mma_f8(tmem + ab * BN, a_d + 2 * j, b_d + 2 * j, idesc, j != 0 ? 1u : 0u);
+          }
           commit<PAIR>(&empty[s]);
           commit<PAIR>(&acc_full[ab]);
         }
