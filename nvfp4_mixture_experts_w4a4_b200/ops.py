@@ -759,8 +759,9 @@ class GraphedMoeFFN:
     CPU); the returned `out_host` is valid once the current stream has reached the replay's
     end (e.g. after torch.cuda.current_stream().synchronize()).
 
-    The graph reads the weights where they were at the capture and keeps them alive.  Values written
-    into them are seen; a call after the layer's weights or settings were replaced raises RuntimeError."""
+    The graph reads the weights where they were at the capture and keeps them alive; values written
+    into them are seen.  An FP8MoeFFN reads its experts at the call, so its graph raises RuntimeError once
+    they, top_k or the launch were replaced; a MoeFFN's goes on with those of the capture."""
 
     def __init__(self, layer: MoeFFN | FP8MoeFFN, T: int, host_io: bool = False):
         dev = layer.w.w13_codes.device
@@ -787,9 +788,10 @@ class GraphedMoeFFN:
                 self.out_host.copy_(self.out, non_blocking=True)
         # the layer's and its experts' tensors and settings (a name with an underscore is a cache)
         self._held = [(vars(o), n, v) for o in (layer, layer.w) for n, v in vars(o).items() if n[0] != "_"]
+        self._checked = self._held if isinstance(layer, FP8MoeFFN) else []
 
     def __call__(self, x: torch.Tensor = None, logits: torch.Tensor = None) -> torch.Tensor:
-        for owner, name, value in self._held:
+        for owner, name, value in self._checked:
             now = owner.get(name)
             if now is not value and not (isinstance(value, int) and now == value):
                 raise RuntimeError(f"the layer's {name} was replaced since the capture: capture it again")
