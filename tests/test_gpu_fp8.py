@@ -932,3 +932,14 @@ def test_weights_written_right_before_a_call(T):
             ops.fp8_quantize(ws[a][2], tile=ops.FP8_BLOCKS, codes=w.w2_codes, scale=w.w2_scale)
         assert torch.equal(layer(x, now), want[a][b]), i
     assert ops.device_status() == 0
+
+
+@pytest.mark.parametrize("T,H,I,E,k", [c for c in CASES if in_tiles(c[0], c[3], c[4])])
+def test_layer_in_tiles_keeps_fp32_rows(T, H, I, E, k):
+    """The bound of the other forms, without layer_reference's allowance for rows that wait in fewer bits."""
+    w = experts(E, I, H, T + E + 1)
+    g = gen(T + 1)
+    x, logits = torch.randn(T, H, generator=g, device="cuda").bfloat16(), torch.randn(T, E, generator=g, device="cuda")
+    ref, bound = layer_reference(w, x, logits, k, False)
+    assert ((ops.FP8MoeFFN(w, k)(x, logits).double() - ref).abs() <= bound).all()
+    assert ops.device_status() == 0
