@@ -82,9 +82,11 @@ bool takes_single(const fp8_moe_ffn_desc& d) {
 
 // The stream of weights in groups of 32 rows: few rows an expert (20 on average at most: most experts
 // are one group, and a 128-row tile would be nearly empty), and a batch short enough that an expert that
-// everyone picks is read from L2 eight times at most.  Measured against the tiles, 512 experts of 2048 x
-// 512, top 10: 100 tokens 60 / 74 us (256 experts, Zipf), 512 tokens with Zipf-popular experts 150 / 136
-// us, which is why the batch is bounded.
+// everyone picks is read from L2 eight times at most.  Stream / tiles, us: 64 experts of 2048 x 512, top 10,
+// with 10, 20 and 30 rows an expert 64 / 71, 68 / 77, 71 / 79, with 40 85 / 80; 64 experts of 4096 x 1024,
+// top 8, with 16, 20, 25 and 32 rows 156 / 175, 161 / 181, 168 / 183, 191 / 186; 8 experts of 2048 x 512, top
+// 2, with 15 to 40 rows within 2 %.  (So 20 is on the safe side of the crossing near 30.)  The batch is bounded
+// because of popular experts: 512 tokens, 512 experts, Zipf 150 / 136.
 bool takes_stream(const fp8_moe_ffn_desc& d) {
   const int64_t P = int64_t(d.T) * d.top_k, touched = P < d.E ? P : d.E;
   return d.T <= 256 && P <= 20 * touched;
@@ -170,7 +172,8 @@ nvfp4moe_status fp8_moe_ffn_forward(const fp8_moe_ffn_desc* desc, const void* x,
   int4* groups = reinterpret_cast<int4*>(ws + L.groups);
   int* counters = L.stream ? i32(L.counters) : nullptr;
   if (prologue_fits(d.T, d.E, d.top_k)) {
-    // one cluster launch for routing and permutation, then x
+    // one cluster launch for routing and permutation, then x (45 tokens, 20 experts of 1040 x 336: 29.5 us, 32.1
+    // with the three launches of larger batches; 33 to 64 tokens, 512 experts of 2048 x 512: within 0.5 %)
     st = launch_prologue(x, logits, d.T, d.H, d.E, d.top_k, 1, 0, nullptr, i32(L.ids), f32(L.w), i32(L.counts),
                          i32(L.offsets), i32(L.padded), i32(L.pair_to_row), i32(L.row_token), i32(L.row_pair),
                          i32(L.tile_expert), i32(L.active), nullptr, 1, nullptr, nullptr, nullptr, nullptr, 0, 0, s);

@@ -14,11 +14,13 @@
 // kb + 1 runs under the additions of block kb.  Per block an SM multiplies for 512 cycles (128 x 256 x
 // 128 at 8192 MACs a cycle) while its eight adding warps read 128 KB of TMEM (256 cycles) and issue 256
 // FMAs a scheduler (256 cycles).  What a block takes is 1000 to 1200 cycles.  Dense: 4096 x 5120 x 17408 in
-// pairs 391 us, 306 with the additions left out; the rest is the way between the MMA and the additions
-// (commit, barrier, read, barrier), and in a long run power (405 to 440 us at 1.57 GHz, 367 in a burst:
-// 1990 TFLOP/s).  Grouped, with experts of 128 rows and more: the loads, 10 TB/s from L2 of which 4.5 come
-// from memory (4096 tokens, 256 experts of 4096 x 1024: the layer 993 us, 928 with the additions left out,
-// the same with three stages as with four, and 6 to 14 % more with prefetches into L2).
+// pairs 366 to 370 us in a burst (1990 TFLOP/s), 425 to 435 in a long run (power: 1.57 GHz).  Of a run of 391,
+// 306 were left without the additions: the rest is the way between the MMA and the additions (commit, barrier,
+// read, barrier).  And 320 tiles on 74 pairs are 4.32 rounds that take the time of five: in the last, 50 pairs
+// have nothing to do, 13.5 % of the time.  Grouped, with experts of 128 rows and more: the loads, 10 TB/s from
+// L2 of which 4.5 come from memory (4096 tokens, 256 experts of 4096 x 1024: gate/up 492 us, down 343; with
+// the additions left out the layer lost 65 of 993 us, three stages were as good as four, and prefetches into L2
+// cost 6 to 14 %).
 //
 //   warp 0      TMA producer: 128 rows of A and BN rows of B, 128 bytes of K each, per stage
 //   warp 1      TMEM owner and MMA issuer
@@ -33,8 +35,9 @@
 // Pairs of CTAs (cta_group::2) take 256 x 256 tiles of large dense products: each loads half of B, a
 // third less to load (2048 x 4096 x 4096: 42.6 us, 46.3 unpaired).  Grouped tiles stay single: an
 // expert's rows rarely fill 256 (gate/up 588 us in pairs, 490 single, 256 experts with 128 rows on
-// average).  Where experts have few rows the weights' rate from memory bounds them (4.5 TB/s, which a
-// stream of 250 MB reaches with nothing else to do).
+// average).  Where experts have few rows their weights come at 4.5 TB/s in these two launches; fp8_layer.cu, which
+// streams gate/up and down weights in one, gets 5.5 to 6, so this is not the memory's own limit: each launch
+// waits for the one before it with nothing in flight (how much of the difference that makes is not measured).
 //
 // Products with few tiles and a long sum split K over the CTAs of a cluster (SPLIT): each adds its
 // share of the blocks, writes its tile to its own shared memory, and the cluster's CTAs sum slices
@@ -934,7 +937,9 @@ nvfp4moe_status launch_fp8_dense(const uint8_t* A, int64_t lda, const float* A_s
   p.M = int(M), p.N = int(N), p.nkb = int(fp8_blocks(K)), p.nsb = int(fp8_blocks(N));
   const int high = plan.pair ? 2 * TM : TM;
   p.n_mt = int((M + high - 1) / high), p.n_nt = int((N + plan.bn - 1) / plan.bn);
-  p.a_box = M <= 96 ? 32 : TM;  // short products load only the rows' 32-row groups that exist
+  // Short products load only the 32-row groups of A that exist: 1 x 17408 x 5120 20.8 us, 26.0 with whole boxes.
+  // With several groups there is no difference (33 to 128 rows of 4096 x 4096 and 17408 x 5120, within 1 %).
+  p.a_box = M <= 96 ? 32 : TM;
   p.sa = A_scale, p.lda_s = lda_s, p.sb = B_scale, p.ldb_s = ldb_s, p.sb_e = 0;
   p.D = D, p.ldd = ldd, p.d_f32 = d_f32;
   const int64_t elt = d_f32 ? 4 : 2;
