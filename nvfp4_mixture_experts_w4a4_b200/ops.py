@@ -773,19 +773,20 @@ class GraphedMoeFFN:
             self.x_host = torch.zeros(T, layer.w.H, dtype=torch.bfloat16).pin_memory()
             self.logits_host = torch.zeros(T, layer.w.E, dtype=torch.float32).pin_memory()
             self.out_host = torch.empty(T, layer.w.H, dtype=torch.bfloat16).pin_memory()
-        side = torch.cuda.Stream(device=dev)
-        side.wait_stream(torch.cuda.current_stream(dev))
-        with torch.cuda.stream(side):
-            layer(self.x, self.logits, out=self.out)  # workspace and kernel attributes set up
-        torch.cuda.current_stream(dev).wait_stream(side)
-        self.graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(self.graph):
-            if host_io:
-                self.x.copy_(self.x_host, non_blocking=True)
-                self.logits.copy_(self.logits_host, non_blocking=True)
-            layer(self.x, self.logits, out=self.out)
-            if host_io:
-                self.out_host.copy_(self.out, non_blocking=True)
+        with torch.cuda.device(dev):  # the layer's, whichever is current
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                layer(self.x, self.logits, out=self.out)  # workspace and kernel attributes set up
+            torch.cuda.current_stream().wait_stream(side)
+            self.graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(self.graph):
+                if host_io:
+                    self.x.copy_(self.x_host, non_blocking=True)
+                    self.logits.copy_(self.logits_host, non_blocking=True)
+                layer(self.x, self.logits, out=self.out)
+                if host_io:
+                    self.out_host.copy_(self.out, non_blocking=True)
         # the layer's and its experts' tensors and settings (a name with an underscore is a cache)
         self._held = [(vars(o), n, v) for o in (layer, layer.w) for n, v in vars(o).items() if n[0] != "_"]
         self._checked = self._held if isinstance(layer, FP8MoeFFN) else []

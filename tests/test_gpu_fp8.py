@@ -943,3 +943,16 @@ def test_layer_in_tiles_keeps_fp32_rows(T, H, I, E, k):
     ref, bound = layer_reference(w, x, logits, k, False)
     assert ((ops.FP8MoeFFN(w, k)(x, logits).double() - ref).abs() <= bound).all()
     assert ops.device_status() == 0
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs a second device")
+def test_on_a_device_that_is_not_current():
+    """Eager and captured calls on the tensors' device, another being current."""
+    with torch.cuda.device(1):
+        w = experts(8, 128, 256, 1)
+        x, logits = torch.randn(4, 256, device="cuda").bfloat16(), torch.randn(4, 8, device="cuda")
+        want = ops.FP8MoeFFN(w, 2)(x, logits)
+    torch.cuda.synchronize(1)
+    layer = ops.FP8MoeFFN(w, 2)
+    assert torch.equal(layer(x, logits), want)
+    assert torch.equal(ops.GraphedMoeFFN(layer, 4)(x, logits), want)
