@@ -420,7 +420,8 @@ nvfp4moe_status moe_ffn_forward(const moe_ffn_desc* desc, const void* x, const f
  * bf16 or fp32 (d_dtype).  Products of one 128-block of K are summed in fp32 by the tensor cores,
  * multiplied by the block's two scales (one after the other where their fp32 product would lose bits
  * or overflow) and added in fp32.  Row pitches: lda, ldb in bytes (multiples of 16, as the base
- * addresses), lda_s, ldb_s, ldd in elements.  M, N, K >= 1 of any size (M or N of 0: nothing to do).  No workspace; the result does not depend on timing.
+ * addresses), lda_s, ldb_s, ldd in elements.  M, N, K >= 1 of any size (M or N of 0: nothing to
+ * do).  No workspace; the result does not depend on timing.
  * ---------------------------------------------------------------------------- */
 enum { NVFP4MOE_FP8_ROWS = 0, NVFP4MOE_FP8_BLOCKS = 1 };
 
